@@ -88,6 +88,16 @@ def _load():
     lib.kda_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
     lib.kda_last_precondition_flags.restype = ctypes.c_uint32
     lib.kda_last_precondition_flags.argtypes = []
+    lib.kda_linear_chunk_fwd_workspace_bytes.restype = sz
+    lib.kda_linear_chunk_fwd_workspace_bytes.argtypes = [i32, i64] + [i32] * 6
+    lib.kda_linear_chunk_fwd.restype = i32
+    lib.kda_linear_chunk_fwd.argtypes = [vp] * 6 + [i32, i64] + [i32] * 7 + [vp, vp, vp, sz, vp]
+    lib.kda_linear_chunk_bwd_workspace_bytes.restype = sz
+    lib.kda_linear_chunk_bwd_workspace_bytes.argtypes = [i32, i64] + [i32] * 8
+    lib.kda_linear_chunk_bwd.restype = i32
+    lib.kda_linear_chunk_bwd.argtypes = [vp] * 8 + [i32, i64] + [i32] * 7 + [vp] * 6 + [sz, vp]
+    lib.kda_linear_decode_step.restype = i32
+    lib.kda_linear_decode_step.argtypes = [vp] * 5 + [i32] * 7 + [vp, vp]
     lib.kda_decode_replay.restype = i32
     lib.kda_decode_replay.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp,
                                       vp, vp]
@@ -526,3 +536,10 @@ def decode_replay(state_in: Optional[torch.Tensor], q: torch.Tensor, k: torch.Te
     if rc != KDA_OK:
         raise KDAError(rc, "kda_decode_replay")
     return out, state_out
+
+
+from .linear import (chunk_linear, linear_chunk_bwd, linear_chunk_bwd_workspace_bytes, linear_chunk_fwd,  # noqa: E402
+                     linear_chunk_fwd_workspace_bytes, linear_decode_step)
+
+__all__ += ["linear_chunk_fwd", "linear_chunk_bwd", "chunk_linear", "linear_decode_step",
+            "linear_chunk_fwd_workspace_bytes", "linear_chunk_bwd_workspace_bytes"]

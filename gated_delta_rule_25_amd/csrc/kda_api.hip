@@ -6,7 +6,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -14,53 +13,12 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_api_util.h"
 #include "kda_internal.h"
 
 namespace {
 
-constexpr int kD = 128;
-
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-};
-
-Range range_of(const void* p, size_t bytes) {
-  Range r;
-  if (p && bytes) {
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    r.hi = r.lo + bytes;
-  }
-  return r;
-}
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-int cu_count_for_current_device() {
-  static std::atomic<int> cache[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
-  if (dev < 64) {
-    int v = cache[dev].load(std::memory_order_relaxed);
-    if (v > 0) return v;
-  }
-  int n = 0;
-  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-size_t elem_size(kda_dtype dt) { return dt == KDA_DTYPE_BF16 ? 2 : 4; }
-
-bool dtype_ok(kda_dtype dt) { return dt == KDA_DTYPE_F32 || dt == KDA_DTYPE_BF16; }
-
-// q, k, v, log_alpha, gate, o and the states move as 16-byte vectors; the
-// rest (beta, cu_seqlens, conv and norm weights, workspace) are read as scalars.
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+using namespace kda::api;
 
 constexpr int kMinAutoSegment = 512;
 #ifndef KDA_PREP_CHUNKS_PER_BLOCK
@@ -166,14 +124,25 @@ Plan make_plan(int num_seqs, int64_t total_tokens, int num_heads, kda_dtype dtyp
 const kda_fused_opts kNoOpts = {nullptr, nullptr, nullptr, nullptr, 1e-6f, 1e-6f, 0, 0, 0};
 constexpr float kBoundedLaMin = -5.f;  // the K3 decay bound the tile paths rely on
 
+// The failed checks of the calling thread's last checked call, for
+// kda_last_precondition_flags().
+thread_local uint32_t t_check_flags = 0;
+
+}  // namespace
+
+namespace kda {
 // Optional precondition checks: the environment variable KDA_DEBUG_CHECKS
-// (read at every call) switches them on; the failed checks of the calling
-// thread's last checked call are kept for kda_last_precondition_flags().
+// (read at every call) switches them on.
 bool debug_checks() {
   const char* e = std::getenv("KDA_DEBUG_CHECKS");
   return e && *e && std::strcmp(e, "0") != 0;
 }
-thread_local uint32_t t_check_flags = 0;
+void set_check_flags(uint32_t flags) { t_check_flags = flags; }
+}  // namespace kda
+
+namespace {
+
+using kda::debug_checks;
 
 // Runs the checks when they are on: KDA_OK to go ahead, otherwise the status to return.
 kda_status checked(const kda::CheckArgs& a, hipStream_t stream) {

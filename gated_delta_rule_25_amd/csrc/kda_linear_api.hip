@@ -1,0 +1,426 @@
+// kda_linear_api.hip — the C ABI of per-head-decay linear attention
+// (include/kda_linear.h): argument validation before anything is enqueued,
+// the launch plan, the launches on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "kda_api_util.h"
+#include "kda_linear.h"
+#include "kda_linear_internal.h"
+
+namespace {
+
+using namespace kda::api;
+
+constexpr size_t kStateBytes = (size_t)kD * kD * sizeof(float);
+// The walk copies rows through 64-bit addresses; the bound is the one of the
+// other prefill calls.
+constexpr int kMaxHeads = 65535;
+// Longest stretch over which the decays' gradient is summed token by token
+// before it is taken from the states again.
+constexpr int64_t kAnchorTokens = 1024;
+constexpr int64_t kMinSegment = 256;
+
+bool linear_sizes_ok(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads) {
+  return num_seqs >= 1 && num_heads >= 1 && num_heads <= kMaxHeads && num_qk_heads >= 1 &&
+         num_heads % num_qk_heads == 0 && total_tokens >= 0 && total_tokens <= (int64_t)INT32_MAX &&
+         (int64_t)num_seqs * num_heads <= (int64_t)INT32_MAX / 4;
+}
+
+struct LinearPlan {
+  bool segmented = false;
+  bool narrow = false;
+  int64_t seg = kAnchorTokens;
+  int64_t slots = 0;  // segments, empty ones included
+  size_t off_fsnap = 0, off_rsnap = 0, off_decay = 0, off_row = 0, off_part = 0, off_share = 0;
+  size_t bytes = 0;
+};
+
+void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
+                     bool backward) {
+  const int64_t units = (int64_t)num_seqs * num_heads;
+  pl.narrow = !backward && units < cus;
+  if (segment_tokens > 0) {
+    pl.segmented = true;
+    pl.seg = segment_tokens;
+  } else if (segment_tokens == 0 && 3 * units < cus) {
+    const int64_t target = (2 * cus + num_heads - 1) / num_heads;
+    int64_t seg = (total_tokens + target - 1) / target;
+    seg = std::max((seg + 63) / 64 * 64, kMinSegment);
+    if ((int64_t)num_seqs * seg < total_tokens) {
+      pl.segmented = true;
+      pl.seg = seg;
+    }
+  }
+  if (pl.segmented) pl.narrow = false;
+  pl.slots = kda::linear_slots(total_tokens, num_seqs, pl.seg);
+}
+
+bool plan_ok(const LinearPlan& pl, int num_heads) {
+  return pl.slots * num_heads <= (int64_t)INT32_MAX / 4;
+}
+
+LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus) {
+  LinearPlan pl;
+  choose_segments(pl, num_seqs, total_tokens, num_heads, segment_tokens, cus, false);
+  if (pl.segmented) {
+    const size_t units = (size_t)pl.slots * num_heads;
+    size_t off = 0;
+    pl.off_fsnap = off;
+    off += units * kStateBytes;
+    pl.off_decay = off;
+    off += align256(units * sizeof(float));
+    pl.bytes = off;
+  }
+  return pl;
+}
+
+// Pieces, each 256-byte aligned: S at the segment boundaries and, segmented,
+// dS at them ([slots][H] states); the segments' decays [slots][H]; r_t's part
+// through the state [T, H]; the per-item sums of a constant decay's gradient;
+// the fp32 gradient [T, H, 128] that shared heads are summed from.
+LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads, int segment_tokens,
+                         bool decay_grad, bool decay_per_head, int cus) {
+  LinearPlan pl;
+  choose_segments(pl, num_seqs, total_tokens, num_heads, segment_tokens, cus, true);
+  const size_t units = (size_t)pl.slots * num_heads;
+  const size_t rows = (size_t)total_tokens * num_heads;
+  size_t off = 0;
+  pl.off_fsnap = off;
+  if (pl.segmented || decay_grad) off += units * kStateBytes;
+  pl.off_rsnap = off;
+  if (pl.segmented) off += units * kStateBytes;
+  pl.off_decay = off;
+  if (pl.segmented) off += align256(units * sizeof(float));
+  pl.off_row = off;
+  if (decay_grad) off += align256(rows * sizeof(float));
+  pl.off_part = off;
+  if (decay_grad && decay_per_head)
+    off += align256((pl.segmented ? units : (size_t)num_seqs * num_heads) * sizeof(double));
+  pl.off_share = off;
+  if (num_qk_heads != num_heads) off += rows * kD * sizeof(float);
+  pl.bytes = off;
+  return pl;
+}
+
+kda_status linear_checked(const float* log_decay, int64_t count, const int32_t* cu, int num_seqs,
+                          int64_t total_tokens, hipStream_t stream) {
+  if (!kda::debug_checks()) return KDA_OK;
+  uint32_t flags = 0;
+  if (kda::run_linear_checks(log_decay, count, cu, num_seqs, total_tokens, stream, &flags) != hipSuccess)
+    return KDA_ERR_HIP;
+  kda::set_check_flags(flags);
+  return flags ? KDA_ERR_PRECONDITION : KDA_OK;
+}
+
+bool all_aligned(const void* const* p, size_t count, uintptr_t a) {
+  for (size_t i = 0; i < count; ++i)
+    if (!aligned(p[i], a)) return false;
+  return true;
+}
+
+// Whether an output meets an input or another output.
+bool any_overlap(const Range* outs, size_t no, const Range* ins, size_t ni) {
+  for (size_t i = 0; i < no; ++i) {
+    for (size_t j = 0; j < ni; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+    for (size_t j = i + 1; j < no; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+// Incoming states of the segments: their own contributions, then the scan.
+hipError_t segment_states(kda::LinearWalkArgs w, const float* init, hipStream_t stream) {
+  w.write_o = false;
+  w.transposed = false;
+  w.narrow = false;
+  w.with_decay_grad = false;
+  hipError_t e = kda::launch_linear_walk(w, stream);
+  if (e != hipSuccess) return e;
+  kda::LinearScanArgs s;
+  std::memset(&s, 0, sizeof(s));
+  s.snap = w.snap;
+  s.seg_decay = w.seg_decay;
+  s.init = init;
+  s.cu = w.cu;
+  s.num_seqs = w.num_seqs;
+  s.total_tokens = w.total_tokens;
+  s.num_heads = w.num_heads;
+  s.seg = w.seg;
+  s.reverse = w.reverse;
+  return kda::launch_linear_scan(s, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_linear_chunk_fwd_workspace_bytes(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads,
+                                            int d_k, int d_v, kda_dtype dtype, int segment_tokens) {
+  if (!linear_sizes_ok(num_seqs, total_tokens, num_heads, num_qk_heads) || d_k != kD || d_v != kD || !dtype_ok(dtype))
+    return 0;
+  if (segment_tokens > 0 && segment_tokens % 64 != 0) return 0;
+  const LinearPlan pl = make_fwd_plan(num_seqs, total_tokens, num_heads, segment_tokens, cu_count_for_current_device());
+  return plan_ok(pl, num_heads) ? pl.bytes : 0;
+}
+
+kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                const float* initial_state, const int32_t* cu_seqlens, int num_seqs,
+                                int64_t total_tokens, int num_heads, int num_qk_heads, int decay_per_head, int d_k,
+                                int d_v, kda_dtype dtype, int segment_tokens, void* o, float* final_state,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (num_seqs < 1 || num_heads < 1 || num_qk_heads < 1 || total_tokens < 0) return KDA_ERR_INVALID_ARG;
+  if (d_k != kD || d_v != kD || !dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
+  if (!linear_sizes_ok(num_seqs, total_tokens, num_heads, num_qk_heads)) return KDA_ERR_INVALID_ARG;
+  if (segment_tokens > 0 && segment_tokens % 64 != 0) return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!q || !k || !v || !log_decay || !o)) return KDA_ERR_INVALID_ARG;
+  {
+    const void* vec[] = {q, k, v, initial_state, o, final_state, workspace};
+    const void* sca[] = {log_decay, cu_seqlens};
+    if (!all_aligned(vec, 7, 16) || !all_aligned(sca, 2, 4)) return KDA_ERR_INVALID_ARG;
+  }
+  const LinearPlan pl = make_fwd_plan(num_seqs, total_tokens, num_heads, segment_tokens, cu_count_for_current_device());
+  if (!plan_ok(pl, num_heads)) return KDA_ERR_INVALID_ARG;
+  if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return KDA_ERR_WORKSPACE;
+
+  const size_t es = elem_size(dtype);
+  const size_t qk = (size_t)total_tokens * num_qk_heads * kD * es, vo = (size_t)total_tokens * num_heads * kD * es;
+  const int64_t decays = decay_per_head ? num_heads : total_tokens * num_heads;
+  const size_t state_bytes = (size_t)num_seqs * num_heads * kStateBytes;
+  const Range r_s0 = range_of(initial_state, initial_state ? state_bytes : 0);
+  const Range r_fs = range_of(final_state, final_state ? state_bytes : 0);
+  const Range r_cu = range_of(cu_seqlens, cu_seqlens ? (size_t)(num_seqs + 1) * sizeof(int32_t) : 0);
+  const Range ins[] = {range_of(q, qk), range_of(k, qk), range_of(v, vo),
+                       range_of(log_decay, (size_t)decays * sizeof(float)), r_cu};
+  const Range outs[] = {range_of(o, vo), r_fs, range_of(workspace, pl.bytes)};
+  if (any_overlap(outs, 3, ins, 5)) return KDA_ERR_INVALID_ARG;
+  if (overlap(outs[0], r_s0) || overlap(outs[2], r_s0)) return KDA_ERR_INVALID_ARG;
+  // final_state may be exactly initial_state (in-place continuation)
+  if (overlap(r_fs, r_s0) && !(r_fs.lo == r_s0.lo && r_fs.hi == r_s0.hi)) return KDA_ERR_INVALID_ARG;
+  {
+    const kda_status cs = linear_checked(log_decay, total_tokens > 0 ? decays : 0, cu_seqlens, num_seqs, total_tokens,
+                                         stream);
+    if (cs != KDA_OK) return cs;
+  }
+
+  char* ws = static_cast<char*>(workspace);
+  kda::LinearWalkArgs w;
+  std::memset(&w, 0, sizeof(w));
+  w.q = q;
+  w.k = k;
+  w.v = v;
+  w.q_heads = w.k_heads = num_qk_heads;
+  w.v_heads = w.x_heads = num_heads;
+  w.log_decay = log_decay;
+  w.decay_per_head = decay_per_head != 0;
+  w.cu = cu_seqlens;
+  w.num_seqs = num_seqs;
+  w.total_tokens = total_tokens;
+  w.num_heads = num_heads;
+  w.bf16 = dtype == KDA_DTYPE_BF16;
+  w.seg = (int)pl.seg;
+  w.segmented = pl.segmented;
+  w.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
+  w.narrow = pl.narrow;
+  w.write_o = true;
+  w.init = initial_state;
+  w.fin = final_state;
+  w.o = o;
+  if (pl.segmented) {
+    w.snap = reinterpret_cast<float*>(ws + pl.off_fsnap);
+    w.seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
+    if (segment_states(w, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  return kda::launch_linear_walk(w, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+size_t kda_linear_chunk_bwd_workspace_bytes(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads,
+                                            int decay_per_head, int need_d_log_decay, int d_k, int d_v,
+                                            kda_dtype dtype, int segment_tokens) {
+  if (!linear_sizes_ok(num_seqs, total_tokens, num_heads, num_qk_heads) || d_k != kD || d_v != kD || !dtype_ok(dtype))
+    return 0;
+  if (segment_tokens > 0 && segment_tokens % 64 != 0) return 0;
+  const LinearPlan pl = make_bwd_plan(num_seqs, total_tokens, num_heads, num_qk_heads, segment_tokens,
+                                      need_d_log_decay != 0, decay_per_head != 0, cu_count_for_current_device());
+  return plan_ok(pl, num_heads) ? pl.bytes : 0;
+}
+
+kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                const float* initial_state, const int32_t* cu_seqlens, const void* d_o,
+                                const float* d_final_state, int num_seqs, int64_t total_tokens, int num_heads,
+                                int num_qk_heads, int decay_per_head, int d_k, int d_v, kda_dtype dtype,
+                                int segment_tokens, void* dq, void* dk, void* dv, float* d_log_decay,
+                                float* d_initial_state, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (num_seqs < 1 || num_heads < 1 || num_qk_heads < 1 || total_tokens < 0) return KDA_ERR_INVALID_ARG;
+  if (d_k != kD || d_v != kD || !dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
+  if (!linear_sizes_ok(num_seqs, total_tokens, num_heads, num_qk_heads)) return KDA_ERR_INVALID_ARG;
+  if (segment_tokens > 0 && segment_tokens % 64 != 0) return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv)) return KDA_ERR_INVALID_ARG;
+  {
+    const void* vec[] = {q, k, v, initial_state, d_o, d_final_state, dq, dk, dv, d_initial_state, workspace};
+    const void* sca[] = {log_decay, cu_seqlens, d_log_decay};
+    if (!all_aligned(vec, 11, 16) || !all_aligned(sca, 3, 4)) return KDA_ERR_INVALID_ARG;
+  }
+  const bool grad = d_log_decay != nullptr, per_head = decay_per_head != 0;
+  const LinearPlan pl = make_bwd_plan(num_seqs, total_tokens, num_heads, num_qk_heads, segment_tokens, grad, per_head,
+                                      cu_count_for_current_device());
+  if (!plan_ok(pl, num_heads)) return KDA_ERR_INVALID_ARG;
+  if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return KDA_ERR_WORKSPACE;
+
+  const size_t es = elem_size(dtype);
+  const size_t qk = (size_t)total_tokens * num_qk_heads * kD * es, vo = (size_t)total_tokens * num_heads * kD * es;
+  const int64_t decays = per_head ? num_heads : total_tokens * num_heads;
+  const size_t state_bytes = (size_t)num_seqs * num_heads * kStateBytes;
+  const Range ins[] = {range_of(q, qk),
+                       range_of(k, qk),
+                       range_of(v, vo),
+                       range_of(log_decay, (size_t)decays * sizeof(float)),
+                       range_of(cu_seqlens, cu_seqlens ? (size_t)(num_seqs + 1) * sizeof(int32_t) : 0),
+                       range_of(initial_state, initial_state ? state_bytes : 0),
+                       range_of(d_o, vo),
+                       range_of(d_final_state, d_final_state ? state_bytes : 0)};
+  const Range outs[] = {range_of(dq, qk),
+                        range_of(dk, qk),
+                        range_of(dv, vo),
+                        range_of(d_log_decay, d_log_decay ? (size_t)decays * sizeof(float) : 0),
+                        range_of(d_initial_state, d_initial_state ? state_bytes : 0),
+                        range_of(workspace, pl.bytes)};
+  if (any_overlap(outs, 6, ins, 8)) return KDA_ERR_INVALID_ARG;
+  {
+    const kda_status cs = linear_checked(log_decay, total_tokens > 0 ? decays : 0, cu_seqlens, num_seqs, total_tokens,
+                                         stream);
+    if (cs != KDA_OK) return cs;
+  }
+
+  char* ws = static_cast<char*>(workspace);
+  const bool shared = num_qk_heads != num_heads;
+  float* share = shared ? reinterpret_cast<float*>(ws + pl.off_share) : nullptr;
+  float* fsnap = reinterpret_cast<float*>(ws + pl.off_fsnap);
+  float* rsnap = reinterpret_cast<float*>(ws + pl.off_rsnap);
+  float* seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
+  double* part = grad && per_head ? reinterpret_cast<double*>(ws + pl.off_part) : nullptr;
+
+  kda::LinearWalkArgs base;
+  std::memset(&base, 0, sizeof(base));
+  base.log_decay = log_decay;
+  base.decay_per_head = per_head;
+  base.cu = cu_seqlens;
+  base.num_seqs = num_seqs;
+  base.total_tokens = total_tokens;
+  base.num_heads = num_heads;
+  base.bf16 = dtype == KDA_DTYPE_BF16;
+  base.seg = (int)pl.seg;
+  base.segmented = pl.segmented;
+  base.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
+  base.seg_decay = seg_decay;
+  base.write_o = true;
+  auto role = [&](kda::LinearWalkArgs& w, const void* a, int ah, const void* b, int bh, const void* c, int ch) {
+    w.q = a;
+    w.q_heads = ah;
+    w.k = b;
+    w.k_heads = bh;
+    w.v = c;
+    w.v_heads = ch;
+  };
+  const int hq = num_qk_heads, hv = num_heads;
+
+  // dq: forwards with S^T
+  kda::LinearWalkArgs w = base;
+  if (pl.segmented) {
+    role(w, nullptr, hq, k, hq, v, hv);
+    w.snap = fsnap;
+    if (segment_states(w, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  role(w, d_o, hv, v, hv, k, hq);
+  w.transposed = true;
+  w.with_decay_grad = grad;
+  w.x = q;
+  w.x_heads = hq;
+  w.init = initial_state;
+  w.fwd_snap = fsnap;
+  w.row_dot = reinterpret_cast<float*>(ws + pl.off_row);
+  w.o = shared ? static_cast<void*>(share) : dq;
+  w.o_f32 = shared;
+  if (kda::launch_linear_walk(w, stream) != hipSuccess) return KDA_ERR_HIP;
+  const int64_t qk_rows = total_tokens * num_qk_heads;
+  if (shared && kda::launch_linear_share_sum(share, dq, qk_rows, hv / hq, base.bf16, stream) != hipSuccess)
+    return KDA_ERR_HIP;
+
+  // dk: backwards with dS^T; it also forms the decays' gradient
+  kda::LinearWalkArgs r = base;
+  r.reverse = true;
+  r.init = d_final_state;
+  if (pl.segmented) {
+    role(r, nullptr, hq, q, hq, d_o, hv);
+    r.snap = rsnap;
+    if (segment_states(r, d_final_state, stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  kda::LinearWalkArgs x = r;
+  role(x, v, hv, d_o, hv, q, hq);
+  x.transposed = true;
+  x.with_decay_grad = grad;
+  x.x = k;
+  x.x_heads = hq;
+  x.fwd_snap = fsnap;
+  x.row_dot = w.row_dot;
+  x.d_log_decay = per_head ? nullptr : d_log_decay;
+  x.d_decay_part = part;
+  x.o = shared ? static_cast<void*>(share) : dk;
+  x.o_f32 = shared;
+  if (kda::launch_linear_walk(x, stream) != hipSuccess) return KDA_ERR_HIP;
+  if (shared && kda::launch_linear_share_sum(share, dk, qk_rows, hv / hq, base.bf16, stream) != hipSuccess)
+    return KDA_ERR_HIP;
+  if (part && kda::launch_linear_decay_sum(part, d_log_decay, base.units, num_heads, stream) != hipSuccess)
+    return KDA_ERR_HIP;
+
+  // dv: backwards with dS
+  role(r, k, hq, q, hq, d_o, hv);
+  r.fin = d_initial_state;
+  r.o = dv;
+  return kda::launch_linear_walk(r, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+kda_status kda_linear_decode_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                                  int num_seqs, int num_heads, int num_qk_heads, int decay_per_head, int d_k, int d_v,
+                                  kda_dtype dtype, void* o, hipStream_t stream) {
+  if (num_seqs < 1 || num_heads < 1 || num_qk_heads < 1) return KDA_ERR_INVALID_ARG;
+  if (d_k != kD || d_v != kD || !dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+  if (!linear_sizes_ok(num_seqs, 0, num_heads, num_qk_heads)) return KDA_ERR_INVALID_ARG;
+  if (!state || !q || !k || !v || !log_decay || !o) return KDA_ERR_INVALID_ARG;
+  const size_t es = elem_size(dtype);
+  if (!aligned(state, 16) || !aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(o, es) ||
+      !aligned(log_decay, 4))
+    return KDA_ERR_INVALID_ARG;
+  const size_t units = (size_t)num_seqs * num_heads;
+  const size_t qk = (size_t)num_seqs * num_qk_heads * kD * es;
+  const int64_t decays = decay_per_head ? num_heads : (int64_t)units;
+  const Range ins[] = {range_of(q, qk), range_of(k, qk), range_of(v, units * kD * es),
+                       range_of(log_decay, (size_t)decays * sizeof(float))};
+  const Range outs[] = {range_of(state, units * kStateBytes), range_of(o, units * kD * es)};
+  if (any_overlap(outs, 2, ins, 4)) return KDA_ERR_INVALID_ARG;
+  {
+    const kda_status cs = linear_checked(log_decay, decays, nullptr, num_seqs, 0, stream);
+    if (cs != KDA_OK) return cs;
+  }
+  kda::LinearDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.state = state;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_decay = log_decay;
+  a.decay_per_head = decay_per_head != 0;
+  a.o = o;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.qk_heads = num_qk_heads;
+  a.bf16 = dtype == KDA_DTYPE_BF16;
+  return kda::launch_linear_decode(a, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,104 @@
+// kda_linear_internal.h — launch descriptors of the per-head-decay linear
+// attention kernels (kda_linear.hip) for the C ABI layer (kda_linear_api.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// Tokens per chunk: one chunk's query, key and value tiles are 16 KiB each.
+constexpr int linear_chunk_len(bool bf16) { return bf16 ? 64 : 32; }
+
+// Segments.  Every sequence is cut into segments of `seg` tokens (a multiple
+// of 64) counted from its own start; segment j of sequence n has the slot
+//   cu[n] / seg + 2 n + j.
+// ceil(L_n / seg) <= floor(cu[n+1] / seg) - floor(cu[n] / seg) + 1, so the
+// slots of two sequences never meet and each sequence has one spare slot
+// behind its last segment (the state it ends with); a slot's sequence is
+// found by bisection, with no table and no prefix sum.
+constexpr int64_t linear_slots(int64_t total_tokens, int num_seqs, int64_t seg) {
+  return total_tokens / seg + 2 * (int64_t)num_seqs;
+}
+
+// One walk of a state over the chunks of a sequence or of a segment.  The
+// recurrence and its three gradients are the same walk with the tensors in
+// other roles:
+//   forward   queries q,  keys k,  values v,  forwards in time,  state S
+//   dq        queries do, keys v,  values k,  forwards,          state S^T
+//   dv        queries k,  keys q,  values do, backwards,         state dS
+//   dk        queries v,  keys do, values q,  backwards,         state dS^T
+struct LinearWalkArgs {
+  const void* q;  // [T, q_heads, 128]: the query role; state head h reads head h / (H / q_heads)
+  const void* k;
+  const void* v;
+  const void* x;  // the tensor whose product with the state's part of the output enters d_log_decay
+  int q_heads, k_heads, v_heads, x_heads;
+  const float* log_decay;  // [T, H], or [H] (decay_per_head)
+  bool decay_per_head;
+  const int32_t* cu;       // [N+1] or null (one sequence)
+  int num_seqs;
+  int64_t total_tokens;
+  int num_heads;
+  bool bf16;
+  int seg;                 // tokens per segment
+  bool segmented;          // work items are (segment, head), else (sequence, head)
+  int64_t units;           // work items
+  bool reverse;            // backwards in time
+  bool transposed;         // the walked state is the transpose of what is stored
+  bool write_o;            // false: only each segment's own contribution to the state
+  bool narrow;             // 64 value columns per workgroup instead of 128
+  bool with_decay_grad;
+  const float* init;       // [N,H,128,128] or null (zero): enters at the sequence's first (reverse: last) token
+  float* fin;              // [N,H,128,128] or null: the state behind the last (reverse: before the first) token
+  float* snap;             // [slots][H][128,128] segmented: incoming states; states pass: contributions (written)
+  float* seg_decay;        // [slots][H] states pass: product of the segment's decays (written)
+  void* o;                 // [T, H, 128] in the I/O dtype, or fp32 (o_f32)
+  bool o_f32;
+  // gradient of the decays
+  float* fwd_snap;         // [slots][H][128,128]: S entering each segment, and behind the last one
+  float* row_dot;          // [T, H]: q_t . dq_t's part through the state (dq walk writes, dk walk reads)
+  float* d_log_decay;      // [T, H] or null (dk walk)
+  double* d_decay_part;    // decay_per_head: [work items] sums (dk walk), else null
+};
+
+struct LinearScanArgs {
+  float* snap;             // contributions in, incoming states out
+  const float* seg_decay;
+  const float* init;       // as above
+  const int32_t* cu;
+  int num_seqs;
+  int64_t total_tokens;
+  int num_heads;
+  int seg;
+  bool reverse;
+};
+
+struct LinearDecodeArgs {
+  float* state;            // [N,H,128,128], in place
+  const void* q;           // [N, qk_heads, 128]
+  const void* k;
+  const void* v;           // [N, H, 128]
+  const float* log_decay;  // [N, H] or [H]
+  bool decay_per_head;
+  void* o;
+  int num_seqs;
+  int num_heads;
+  int qk_heads;
+  bool bf16;
+};
+
+hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream);
+hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream);
+// dst[t][g] = sum over the `share` heads of group g of src[t][g share + i], fp32 to the I/O dtype.
+hipError_t launch_linear_share_sum(const float* src, void* dst, int64_t rows, int share, bool bf16,
+                                   hipStream_t stream);
+// dst[h] = sum over the work items u with u % num_heads = h of part[u], in order.
+hipError_t launch_linear_decay_sum(const double* part, float* dst, int64_t units, int num_heads, hipStream_t stream);
+hipError_t launch_linear_decode(const LinearDecodeArgs& a, hipStream_t stream);
+// Checks the documented input ranges (log_decay <= 0 and not NaN; cu_seqlens)
+// on `stream`, waits, and returns the KDA_CHECK_* bits that failed.
+hipError_t run_linear_checks(const float* log_decay, int64_t count, const int32_t* cu, int num_seqs,
+                             int64_t total_tokens, hipStream_t stream, uint32_t* flags);
+
+}  // namespace kda
