@@ -31,6 +31,7 @@
 // are fp64 (a difference of two sums decides every factor).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_chunk_util.h"
@@ -85,61 +86,72 @@ __device__ __forceinline__ int64_t slot_of(int n, int64_t bos, int seg, int64_t 
 }
 
 // ---- LDS tiles ------------------------------------------------------------
-// A tile holds C tokens x 128 channels, row-major, its 16-byte units XOR-ed
-// with the row (mod 16) so that the 16 rows a matrix-core operand reads at
-// one channel fall on different banks.
-template <typename E>
+// A tile holds C tokens x W channels, row-major, its 16-byte units XOR-ed
+// with the row so that the 16 rows a matrix-core operand reads at one channel
+// fall on different banks.
+template <typename E, int W>
 __device__ __forceinline__ int tile_at(int row, int ch) {
-  constexpr int U = 16 / (int)sizeof(E);  // elements per unit
-  return row * D + (((ch / U) ^ (row & 15)) * U) + (ch % U);
+  constexpr int U = 16 / (int)sizeof(E);                  // elements per unit
+  constexpr int M = (W / U < 16 ? W / U : 16) - 1;
+  return row * W + (((ch / U) ^ (row & M)) * U) + (ch % U);
 }
 
 // operand with the channels ch .. ch+7 of a row
 __device__ __forceinline__ void ld_row(Frag<__bf16>& f, const __bf16* t, int row, int ch) {
-  f.v = *reinterpret_cast<const bf16x8*>(t + tile_at<__bf16>(row, ch));
+  f.v = *reinterpret_cast<const bf16x8*>(t + tile_at<__bf16, D>(row, ch));
 }
 __device__ __forceinline__ void ld_row(Frag<float>& f, const float* t, int row, int ch) {
-  f.lo = *reinterpret_cast<const f32x4*>(t + tile_at<float>(row, ch));
-  f.hi = *reinterpret_cast<const f32x4*>(t + tile_at<float>(row, ch + 4));
+  f.lo = *reinterpret_cast<const f32x4*>(t + tile_at<float, D>(row, ch));
+  f.hi = *reinterpret_cast<const f32x4*>(t + tile_at<float, D>(row, ch + 4));
 }
 
-// operand of column ch (one per lane of 16) over the rows row .. row+7.
-// bf16: the transposing LDS read hands each lane of 16 one column of a
-// 4-row x 16-channel block, whose rows the lanes 4r .. 4r+3 address.
-__device__ __forceinline__ void ld_col(Frag<__bf16>& f, const __bf16* t, int row, int ch0, int l16) {
+// Operands whose contraction runs over a chunk's tokens: 32 deep in bf16
+// (eight tokens a lane, the tokens 8 g ..), 16 deep in fp32 (four, 4 g ..).
+template <typename E>
+struct Tok;
+template <>
+struct Tok<__bf16> {
+  using F = Frag<__bf16>;
+  static constexpr int N = 8;
+};
+template <>
+struct Tok<float> {
+  using F = Frag16<float>;
+  static constexpr int N = 4;
+};
+__device__ __forceinline__ f32x4 mma_tok(f32x4 acc, const Frag<__bf16>& a, const Frag<__bf16>& b) {
+  return mma(acc, a, b);
+}
+__device__ __forceinline__ f32x4 mma_tok(f32x4 acc, const Frag16<float>& a, const Frag16<float>& b) {
+  return mma16(acc, a, b);
+}
+// column ch0 + l16 over the lane's tokens.  bf16: the transposing LDS read
+// hands each lane of 16 one column of a 4-row x 16-channel block, whose rows
+// the lanes 4r .. 4r+3 address.
+template <int W>
+__device__ __forceinline__ void ld_col(Frag<__bf16>& f, const __bf16* t, int ch0, int l16, int g) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const int r = row + (l16 >> 2), c = ch0 + 4 * (l16 & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16>(r, c)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16>(r + 4, c)));
+  const int r = 8 * g + (l16 >> 2), c = ch0 + 4 * (l16 & 3);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16, W>(r, c)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16, W>(r + 4, c)));
   const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
   f.v = (bf16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 }
-__device__ __forceinline__ void ld_col(Frag<float>& f, const float* t, int row, int ch0, int l16) {
+template <int W>
+__device__ __forceinline__ void ld_col(Frag16<float>& f, const float* t, int ch0, int l16, int g) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.lo[i] = t[tile_at<float>(row + i, ch0 + l16)];
-    f.hi[i] = t[tile_at<float>(row + 4 + i, ch0 + l16)];
-  }
+  for (int i = 0; i < 4; ++i) f.v[i] = t[tile_at<float, W>(4 * g + i, ch0 + l16)];
 }
-
+// a row of the pair matrix over the lane's tokens (rows of 64 bytes: a wave
+// reads 16 of them whole)
+__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const __bf16* t, int row, int g) {
+  f.v = *reinterpret_cast<const bf16x8*>(t + row * 32 + 8 * g);
+}
+__device__ __forceinline__ void ld_pair(Frag16<float>& f, const float* t, int row, int g) {
+  f.v = *reinterpret_cast<const f32x4*>(t + row * 16 + 4 * g);
+}
 __device__ __forceinline__ float frag_get(const Frag<__bf16>& f, int i) { return (float)f.v[i]; }
-__device__ __forceinline__ float frag_get(const Frag<float>& f, int i) { return i < 4 ? f.lo[i] : f.hi[i - 4]; }
-
-// The pair matrix in LDS: C rows of 128 bytes, 16-byte units XOR-ed with the row (mod 8).
-template <typename E, int C>
-__device__ __forceinline__ int pair_at(int row, int col) {
-  constexpr int U = 16 / (int)sizeof(E);
-  return row * C + (((col / U) ^ (row & 7)) * U) + (col % U);
-}
-template <int C>
-__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const __bf16* t, int row, int col) {
-  f.v = *reinterpret_cast<const bf16x8*>(t + pair_at<__bf16, C>(row, col));
-}
-template <int C>
-__device__ __forceinline__ void ld_pair(Frag<float>& f, const float* t, int row, int col) {
-  f.lo = *reinterpret_cast<const f32x4*>(t + pair_at<float, C>(row, col));
-  f.hi = *reinterpret_cast<const f32x4*>(t + pair_at<float, C>(row, col + 4));
-}
+__device__ __forceinline__ float frag_get(const Frag16<float>& f, int i) { return f.v[i]; }
 
 // x as the sum of NS operands (bf16: NS terms of 8 bits each; fp32: itself).
 template <int NS>
@@ -160,54 +172,82 @@ __device__ __forceinline__ void split(Frag<float> (&f)[NS], const float (&x)[8])
   static_assert(NS == 1, "fp32 operands are exact");
   frag_from_f32(f[0], x);
 }
+template <int NS>
+__device__ __forceinline__ void split(Frag16<float> (&f)[NS], const float (&x)[4]) {
+  static_assert(NS == 1, "fp32 operands are exact");
+  f[0].v = (f32x4){x[0], x[1], x[2], x[3]};
+}
 
-template <typename E, int NX>
+// Every wave's LDS writes land before any wave goes on.  (Not __syncthreads():
+// its fence would also wait for the copies into LDS that the loader wave has
+// in flight for later chunks.)
+__device__ __forceinline__ void chunk_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename E, int CT, bool DG>
 struct WalkLayout {
-  static constexpr int C = sizeof(E) == 2 ? 64 : 32;
-  static constexpr int TILE = C * D * (int)sizeof(E);  // 16 KiB
-  static constexpr int NTILE = 3 + NX;                 // query, key, value[, x]
-  static constexpr int PAIR = 2 * NTILE * TILE;        // two chunks in flight
-  static constexpr int SUM = PAIR + C * C * (int)sizeof(E);  // double [2][C] prefix sums (log2)
-  static constexpr int ROW = SUM + 2 * C * 8;          // float [2][C] factor of the state in row t
-  static constexpr int WGT = ROW + 2 * C * 4;          // float [2][C] factor of token t in the state
-  static constexpr int GAM = WGT + 2 * C * 4;          // float [2]
-  static constexpr int ANC = GAM + 16;                 // float [2][4] <S, dS> by wave
-  static constexpr int RX = ANC + 32;                  // float [2][4][C] state part . x by wave
-  static constexpr int RR = RX + (NX ? 2 * 4 * C * 4 : 0);  // float [2][4][C] pair sums of the keys by wave
-  static constexpr int RC = RR + (NX ? 2 * 4 * C * 4 : 0);  // float [2][2][C] pair sums of the queries
-  static constexpr int BYTES = RC + (NX ? 2 * 2 * C * 4 : 0);
+  static constexpr int C = linear_chunk_len(sizeof(E) == 2);
+  static constexpr int ES = (int)sizeof(E);
+  static constexpr int TILE = C * D * ES;              // 8 KiB: a query, key or x tile
+  static constexpr int VW = 64 * CT;                   // value columns of the workgroup
+  static constexpr int VTILE = C * VW * ES;
+  static constexpr int K = TILE, V = 2 * TILE, X = V + VTILE;
+  static constexpr int SET = X + (DG ? TILE : 0);      // the tiles of a chunk
+  static constexpr int NBUF = DG ? 4 : CT == 2 ? 5 : 6;  // chunks in LDS
+  static constexpr int COPIES = SET / 1024;            // copy instructions per chunk
+  static constexpr int PAIR = NBUF * SET;              // E [2][C][C]
+  static constexpr int SUM = PAIR + 2 * C * C * ES;    // float [4][2][C] prefix sums (log2), high and low part
+  static constexpr int ROW = SUM + 4 * 2 * C * 4;      // float [4][C] factor of the state in row t
+  static constexpr int WGT = ROW + 4 * C * 4;          // float [4][C] factor of token t in the state
+  static constexpr int GAM = WGT + 4 * C * 4;          // float [4] factor of the state over the chunk
+  static constexpr int ANC = GAM + 16;                 // float [4][4] <S, dS> by compute wave
+  static constexpr int RX = ANC + 64;                  // float [4][4][C] state part . x by compute wave
+  static constexpr int RR = RX + (DG ? 16 * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
+  static constexpr int RC = RR + (DG ? 8 * C * 4 : 0);   // float [4][C] pair sums of the queries
+  static constexpr int BYTES = RC + (DG ? 4 * C * 4 : 0);
 };
 
 // ---------------------------------------------------------------------------
-// The walk.  Four compute waves and a loader wave per (sequence or segment,
-// head, block of 64 CT value columns).  Compute wave w owns 16 CT value
-// columns and keeps its [128 x 16 CT] slice of the state in matrix-core
-// accumulators (fp32) over the whole walk; accumulators of two stacked tiles
-// are an operand of the next product as they are.  Per chunk:
-//   1. the pair matrix: wave w forms the products of one 16-query tile with
-//      the keys up to it, scales them by e^{G_i - G_j} and leaves them in LDS;
-//   2. outputs, transposed (rows = value columns), so that a lane stores four
-//      consecutive columns: S^T q, scaled by e^{G_i}, plus the pair matrix
-//      times v;
-//   3. S <- e^{G_C} S + k^T (e^{G_C - G_j} v_j), v read once for 2 and 3.
-// The loader wave copies the next chunk's tiles from global memory straight
-// into the other half of LDS and forms the decays' prefix sums, so that the
-// compute waves never wait behind a copy of their own.  Two barriers per chunk.
+// The walk.  Eight waves per (sequence or segment, head, block of 64 CT value
+// columns), in four roles, meeting at one barrier per chunk:
+//   waves 0-3  compute: wave w owns 16 CT value columns and keeps its
+//              [128 x 16 CT] slice of the state in matrix-core accumulators
+//              (fp32) over the whole walk; accumulators of two stacked tiles
+//              are an operand of the next product as they are.  For chunk c:
+//              the outputs, transposed (rows = value columns), so that a lane
+//              stores four consecutive columns: S^T q, scaled by e^{G_i}, plus
+//              the pair matrix times v; then S <- e^{G_C} S + k^T (e^{G_C - G_j} v_j).
+//   waves 4-5  pair matrix of chunk c + 1, one 16-query tile each: the
+//              products with the keys up to it, scaled by e^{G_i - G_j}
+//   wave 6     the decays: prefix sums and factors of chunk c + 2; with DG the
+//              decays' gradient of chunk c - 1
+//   wave 7     copies tiles from global memory straight into LDS, NBUF - 1
+//              chunks ahead of the compute waves, which therefore never wait
+//              behind a copy of their own
+// One compute and one other wave share each SIMD.  Chunks are 32 tokens (16 in
+// fp32): with 64 the tiles of only two chunks fit beside the ones in use, and
+// the copies' latency showed.
 // REV walks backwards in time: the pair matrix is upper triangular and the
 // factors of rows and of tokens change places.
 // DG (the decays' gradient): x is q in the dq walk and k in the dk walk.
 // ---------------------------------------------------------------------------
 template <typename E, int CT, bool REV, bool TR, bool OUT, bool DG>
-__global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p) {
-  using L = WalkLayout<E, DG ? 1 : 0>;
-  constexpr int C = L::C, NT = C / 16, KT = C / 32, ES = (int)sizeof(E);
+__global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p) {
+  using L = WalkLayout<E, CT, DG>;
+  using TF = typename Tok<E>::F;
+  constexpr int TN = Tok<E>::N;
+  constexpr int C = L::C, NT = C / 16, ES = L::ES, NBUF = L::NBUF;
   constexpr bool BF = ES == 2;
   constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values
   constexpr int NSS = (BF && DG) ? 3 : 1;      // terms of the state in the outputs' product
   constexpr bool DK = DG && REV;               // dk walk: forms the decays' gradient
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
+  static_assert(C == 4 * TN, "one token step per chunk");
   extern __shared__ __align__(16) unsigned char smem[];
-  double* sSum = reinterpret_cast<double*>(smem + L::SUM);
+  float* sSum = reinterpret_cast<float*>(smem + L::SUM);
   float* sRow = reinterpret_cast<float*>(smem + L::ROW);
   float* sWgt = reinterpret_cast<float*>(smem + L::WGT);
   float* sGam = reinterpret_cast<float*>(smem + L::GAM);
@@ -215,9 +255,9 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
   float* sRX = reinterpret_cast<float*>(smem + L::RX);
   float* sRR = reinterpret_cast<float*>(smem + L::RR);
   float* sRC = reinterpret_cast<float*>(smem + L::RC);
-  E* sP = reinterpret_cast<E*>(smem + L::PAIR);
 
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l16 = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr int CB = 2 / CT;  // column blocks of a head
   // blocks b and b + 8 run on the same XCD: a head's column blocks share its L2
   const int64_t slot8 = blockIdx.x >> 3;
@@ -259,36 +299,62 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
   const int nch = (int)((te - tb + C - 1) / C);
   const size_t nh = (size_t)n * H + h;
   auto chunk_of = [&](int ci) { return REV ? nch - 1 - ci : ci; };
+  auto tiles = [&](int ci) { return smem + (ci % NBUF) * L::SET; };
+  // Iteration ci (from -1): compute waves on chunk ci, pair waves on ci + 1,
+  // decay wave on ci + 2 and back on ci - 1, loader on ci + NBUF - 1.
 
-  if (wv == 4) {
-    // ---- loader wave ----
-    auto copy_tile = [&](const void* src, int heads, int64_t t0, int nv, unsigned char* dst) {
-      const int hh = h / (H / heads);
-      const char* base = static_cast<const char*>(src) + ((size_t)t0 * heads + hh) * (D * ES);
-      const size_t stride = (size_t)heads * (D * ES);
-      constexpr int RP = 1024 / (D * ES);  // rows per 1 KiB piece
-      constexpr int UR = 64 / RP;          // 16-byte units per row
+  if (wv == 7) {
+    // ---- loader ----
+    // 1 KiB pieces, 16 bytes a lane; the lanes' offsets are the same in every
+    // chunk.  Rows behind the end lie outside the buffer view and arrive as
+    // zeros.
+    auto copy_tile = [&](auto width, const void* src, int heads, int ch0, int64_t t0, int nv, unsigned char* dst) {
+      constexpr int W = decltype(width)::value;
+      constexpr int NPC = C * W * ES / 1024;   // pieces
+      constexpr int UR = W * ES / 16;          // 16-byte units per row
+      constexpr int RP = 64 / UR;              // rows per piece
+      constexpr int M = (UR < 16 ? UR : 16) - 1;
+      const uint32_t stride = (uint32_t)heads * (D * ES);
+      const char* base = static_cast<const char*>(src) + ((size_t)t0 * heads + h / (H / heads)) * (D * ES);
+      const Rsrc rs = make_rsrc(base, (uint32_t)(nv - 1) * stride + D * ES);
+      uint32_t row = (uint32_t)(lane / UR) * stride + ch0 * ES;
 #pragma unroll
-      for (int i = 0; i < L::TILE / 1024; ++i) {
-        const int row = i * RP + lane / UR;
-        const int unit = (lane % UR) ^ (row & 15);
-        // rows behind the end repeat the last one: their factors are zero
-        const char* s = base + (size_t)min(row, nv - 1) * stride + unit * 16;
-        __builtin_amdgcn_global_load_lds(s, (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, 0, 0);
+      for (int i = 0; i < NPC; ++i) {
+        const uint32_t unit = (uint32_t)(((lane % UR) ^ ((i * RP + lane / UR) & M)) * 16);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + i * 1024), 16,
+                                                 (int)(row + unit), 0, 0, 0);
+        row += RP * stride;
       }
     };
     auto copy_chunk = [&](int ci) {
       const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
       const int nv = (int)min((int64_t)C, te - t0);
-      unsigned char* dst = smem + (ci & 1) * (L::NTILE * L::TILE);
-      if (OUT) copy_tile(p.q, p.q_heads, t0, nv, dst);
-      copy_tile(p.k, p.k_heads, t0, nv, dst + L::TILE);
-      copy_tile(p.v, p.v_heads, t0, nv, dst + 2 * L::TILE);
-      if constexpr (DG) copy_tile(p.x, p.x_heads, t0, nv, dst + 3 * L::TILE);
+      unsigned char* dst = tiles(ci);
+      using Whole = std::integral_constant<int, D>;
+      using Block = std::integral_constant<int, L::VW>;
+      if (OUT) copy_tile(Whole{}, p.q, p.q_heads, 0, t0, nv, dst);
+      copy_tile(Whole{}, p.k, p.k_heads, 0, t0, nv, dst + L::K);
+      copy_tile(Block{}, p.v, p.v_heads, cb * L::VW, t0, nv, dst + L::V);
+      if constexpr (DG) copy_tile(Whole{}, p.x, p.x_heads, 0, t0, nv, dst + L::X);
     };
+    constexpr int PER = L::COPIES - (OUT ? 0 : L::TILE / 1024);  // copies per chunk
+    for (int ci = 0; ci < NBUF - 1 && ci < nch; ++ci) copy_chunk(ci);
+    for (int ci = -1; ci < nch; ++ci) {
+      // chunk ci + 1 has landed; the ones behind it may be in flight
+      if (ci + NBUF - 2 < nch) __builtin_amdgcn_s_waitcnt(vmcnt_wait((NBUF - 3) * PER < 63 ? (NBUF - 3) * PER : 63));
+      else __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+      chunk_barrier();
+      if (ci >= 0 && ci + NBUF - 1 < nch) copy_chunk(ci + NBUF - 1);
+    }
+    if constexpr (DG) chunk_barrier();
+    return;
+  }
+
+  if (wv == 6) {
+    // ---- decays ----
     auto load_decay = [&](int ci) -> float {
       const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
-      if (lane >= C || t >= te) return 0.f;
+      if (ci >= nch || lane >= C || t >= te) return 0.f;
       return p.decay_per_head ? p.log_decay[h] : p.log_decay[(size_t)t * H + h];
     };
     double log_total = 0.0;
@@ -303,83 +369,74 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
       const double tot = __shfl(s, C - 1);
       log_total += tot;
       const float head = exp2_fast((float)s), tail = exp2_fast((float)(tot - s));
+      const int b = ci & 3;
       if (lane < C) {
-        const int b = (ci & 1) * C + lane;
-        sSum[b] = s;
-        sRow[b] = REV ? tail : head;
-        sWgt[b] = t < te ? (REV ? head : tail) : 0.f;
+        const float hi = (float)s;
+        sSum[b * 2 * C + lane] = hi;
+        sSum[b * 2 * C + C + lane] = (float)(s - (double)hi);
+        sRow[b * C + lane] = REV ? tail : head;
+        sWgt[b * C + lane] = t < te ? (REV ? head : tail) : 0.f;
       }
-      if (lane == 0) sGam[ci & 1] = exp2_fast((float)tot);
+      if (lane == 0) sGam[b] = exp2_fast((float)tot);
     };
-    // the decays' gradient of chunk ci from the compute waves' sums
+    // the decays' gradient of a chunk from the other waves' sums
     double flow = 0.0;   // D behind the chunk
     double dsum = 0.0;
     auto finish = [&](int ci, float rdot) {
-      if constexpr (DG) {
-        const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
-        const bool in = lane < C && t0 + lane < te;
-        const int b = ci & 1;
-        float part = 0.f;
-        if (lane < C)
+      const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+      const bool in = lane < C && t0 + lane < te;
+      const int b = ci & 3;
+      float part = 0.f;
+      if (lane < C)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) part += sRX[(b * 4 + w) * C + lane];
-        if constexpr (!REV) {
-          if (in) p.row_dot[(size_t)(t0 + lane) * H + h] = part;
-        } else {
-          float keys = 0.f, queries = 0.f;
-          if (lane < C) {
+        for (int w = 0; w < 4; ++w) part += sRX[(b * 4 + w) * C + lane];
+      if constexpr (!REV) {
+        if (in) p.row_dot[(size_t)(t0 + lane) * H + h] = part;
+      } else {
+        float keys = 0.f, queries = 0.f;
+        if (lane < C) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) keys += sRR[(b * 4 + w) * C + lane];
-            queries = sRC[(b * 2 + 0) * C + lane] + (NT == 2 ? sRC[(b * 2 + 1) * C + lane] : 0.f);
-          }
-          const int64_t tend = min(te, t0 + C);
-          if (tend == te || (tend - bos) % p.seg == 0)
-            flow = (double)sAnc[b * 4] + (double)sAnc[b * 4 + 1] + (double)sAnc[b * 4 + 2] + (double)sAnc[b * 4 + 3];
-          double s = in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0;
-#pragma unroll
-          for (int m = 1; m < C; m <<= 1) {
-            const double o = __shfl_down(s, m);
-            if (lane + m < C) s += o;
-          }
-          const double d = flow + s;
-          if (in) {
-            if (p.d_log_decay) p.d_log_decay[(size_t)(t0 + lane) * H + h] = (float)d;
-            dsum += d;
-          }
-          flow += __shfl(s, 0);
+          for (int w = 0; w < NT; ++w) keys += sRR[(b * 2 + w) * C + lane];
+          queries = sRC[b * C + lane];
         }
+        const int64_t tend = min(te, t0 + C);
+        if (tend == te || (tend - bos) % p.seg == 0)
+          flow = (double)sAnc[b * 4] + (double)sAnc[b * 4 + 1] + (double)sAnc[b * 4 + 2] + (double)sAnc[b * 4 + 3];
+        double s = in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0;
+#pragma unroll
+        for (int m = 1; m < C; m <<= 1) {
+          const double o = __shfl_down(s, m);
+          if (lane + m < C) s += o;
+        }
+        const double d = flow + s;
+        if (in) {
+          if (p.d_log_decay) p.d_log_decay[(size_t)(t0 + lane) * H + h] = (float)d;
+          dsum += d;
+        }
+        flow += __shfl(s, 0);
       }
     };
     auto load_rdot = [&](int ci) -> float {
       if constexpr (DK) {
         const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
-        if (lane < C && t < te) return p.row_dot[(size_t)t * H + h];
+        if (ci >= 0 && lane < C && t < te) return p.row_dot[(size_t)t * H + h];
       }
       return 0.f;
     };
-    if (nch > 0) {
-      put_decay(0, load_decay(0));
-      copy_chunk(0);
-    }
-    float la_next = nch > 1 ? load_decay(1) : 0.f;
-    float rdot_cur = 0.f;
-    for (int ci = 0; ci < nch; ++ci) {
-      __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
-      __syncthreads();  // chunk ci is in LDS; every wave is done with chunk ci - 1
-      const float la = la_next;
-      const float rdot_prev = rdot_cur;
-      if (ci + 2 < nch) la_next = load_decay(ci + 2);
-      rdot_cur = load_rdot(ci);
-      if (ci + 1 < nch) {
-        copy_chunk(ci + 1);
-        put_decay(ci + 1, la);
-      }
-      if (ci > 0) finish(ci - 1, rdot_prev);
-      if (OUT) __syncthreads();  // the pair matrix
+    if (nch > 0) put_decay(0, load_decay(0));
+    float la = load_decay(1), rdot = 0.f;
+    for (int ci = -1; ci < nch; ++ci) {
+      chunk_barrier();
+      const float la_next = load_decay(ci + 3), rdot_next = load_rdot(ci);
+      if (ci + 2 < nch) put_decay(ci + 2, la);
+      if constexpr (DG)
+        if (ci > 0) finish(ci - 1, rdot);
+      la = la_next;
+      rdot = rdot_next;
     }
     if constexpr (DG) {
-      __syncthreads();
-      if (nch > 0) finish(nch - 1, rdot_cur);
+      chunk_barrier();
+      if (nch > 0) finish(nch - 1, rdot);
       if constexpr (REV) {
         if (p.d_decay_part) {
 #pragma unroll
@@ -392,8 +449,91 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
     return;
   }
 
-  // ---- compute waves ----
-  const int col0 = cb * (64 * CT) + 16 * CT * wv;
+  if (wv >= 4) {
+    // ---- pair matrix of chunk ci + 1, keys in rows: lane = query, four consecutive keys ----
+    const int rt = wv - 4;
+    const int q = 16 * rt + l16;
+    for (int ci = -1; ci < nch; ++ci) {
+      chunk_barrier();
+      if (!OUT || rt >= NT || ci + 1 >= nch) continue;
+      const unsigned char* buf = tiles(ci + 1);
+      const E* sQ = reinterpret_cast<const E*>(buf);
+      const E* sK = reinterpret_cast<const E*>(buf + L::K);
+      const E* sV = reinterpret_cast<const E*>(buf + L::V);
+      const E* sX = reinterpret_cast<const E*>(buf + L::X);
+      E* sP = reinterpret_cast<E*>(smem + L::PAIR) + ((ci + 1) & 1) * (C * C);
+      const int b = (ci + 1) & 3;
+      const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
+      const int nv = (int)min((int64_t)C, te - t0);
+      Frag<E> fq[4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], sQ, q, 32 * ks + 8 * g);
+      Frag<E> fx[DK ? 4 : 1];
+      if constexpr (DK)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], sX, q, 32 * ks + 8 * g);
+      const float* gs = sSum + b * 2 * C;
+      const float gq = gs[q], gq_lo = gs[C + q];
+      float csum = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < NT; ++kt) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rsum = {0.f, 0.f, 0.f, 0.f};
+        // a tile beyond the triangle is zero
+        if (REV ? kt >= rt : kt <= rt) {
+          f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            Frag<E> fk;
+            ld_row(fk, sK, 16 * kt + l16, 32 * ks + 8 * g);
+            acc = mma(acc, fk, fq[ks]);
+          }
+          if constexpr (DK)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              Frag<E> fv;
+              ld_row(fv, sV, 16 * kt + l16, 32 * ks + 8 * g);
+              acc2 = mma(acc2, fv, fx[ks]);
+            }
+          const f32x4 gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
+          const f32x4 gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = 16 * kt + 4 * g + i;
+            const bool on = REV ? (k >= q && k < nv) : k <= q;
+            const float d = (gq - gk[i]) + (gq_lo - gk_lo[i]);
+            const float e = acc[i] * exp2_fast(REV ? -d : d);
+            const float x = on ? e : 0.f;
+            if constexpr (DK) {
+              const float f = (on && k != q) ? x * acc2[i] : 0.f;
+              rsum[i] = f;
+              csum += f;
+            }
+            acc[i] = x;
+          }
+        }
+        store_row4(sP + q * C + 16 * kt + 4 * g, acc);
+        if constexpr (DK) {
+          // over the 16 queries of the tile
+#pragma unroll
+          for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rsum[i] += __shfl_xor(rsum[i], m);
+          if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + rt) * C + 16 * kt + 4 * g) = rsum;
+        }
+      }
+      if constexpr (DK) {
+        csum += __shfl_xor(csum, 16);
+        csum += __shfl_xor(csum, 32);
+        if (g == 0) sRC[b * C + q] = csum;
+      }
+    }
+    if constexpr (DG) chunk_barrier();
+    return;
+  }
+
+  // ---- compute ----
+  const int vc0 = 16 * CT * wv;          // first value column within the block
+  const int col0 = cb * L::VW + vc0;     // and within the head
   // state element (row, column) of this walk in a stored state
   auto state_at = [&](int row, int col) { return TR ? col * D + row : row * D + col; };
   auto load_state = [&](const float* src, f32x4 (&s)[CT][8]) {
@@ -443,16 +583,18 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
         for (int rt = 0; rt < 8; ++rt) accS[c][rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
   }
+  chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
-    const unsigned char* buf = smem + (ci & 1) * (L::NTILE * L::TILE);
+    const unsigned char* buf = tiles(ci);
     const E* sQ = reinterpret_cast<const E*>(buf);
-    const E* sK = reinterpret_cast<const E*>(buf + L::TILE);
-    const E* sV = reinterpret_cast<const E*>(buf + 2 * L::TILE);
-    const E* sX = reinterpret_cast<const E*>(buf + 3 * L::TILE);
-    const int b = ci & 1;
+    const E* sK = reinterpret_cast<const E*>(buf + L::K);
+    const E* sV = reinterpret_cast<const E*>(buf + L::V);
+    const E* sX = reinterpret_cast<const E*>(buf + L::X);
+    const E* sP = reinterpret_cast<const E*>(smem + L::PAIR) + (ci & 1) * (C * C);
+    const int b = ci & 3;
 
     // what the decays' gradient needs of the states at segment boundaries
     if constexpr (DG && !REV) {
@@ -478,93 +620,13 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
         if (lane == 0) sAnc[b * 4 + wv] = dot;
       }
     }
-    __syncthreads();  // chunk ci is in LDS
+    chunk_barrier();
 
-    const double* gs = sSum + b * C;
+    TF fv[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) ld_col<L::VW>(fv[c], sV, vc0 + 16 * c, l16, g);
     if constexpr (OUT) {
-      // ---- 1: pair matrix, keys in rows: lane = query, four consecutive keys ----
-      const int rt = NT == 4 ? wv : wv >> 1;
-      Frag<E> fq[4];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], sQ, 16 * rt + l16, 32 * ks + 8 * g);
-      Frag<E> fx[DK ? 4 : 1];
-      if constexpr (DK)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], sX, 16 * rt + l16, 32 * ks + 8 * g);
-      const int q = 16 * rt + l16;
-      const double gq = gs[q];
-      float csum = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < (NT == 4 ? NT : 1); ++kk) {
-        const int kt = NT == 4 ? kk : (wv & 1);
-        // tiles beyond the triangle that share a 32-deep step with it are zero
-        const bool tri = REV ? kt >= rt : kt <= rt;
-        const bool use = REV ? kt >= (rt & ~1) : kt <= (rt | 1);
-        f32x4 rsum = {0.f, 0.f, 0.f, 0.f};
-        if (use) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          if (tri) {
-            f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              Frag<E> fk;
-              ld_row(fk, sK, 16 * kt + l16, 32 * ks + 8 * g);
-              acc = mma(acc, fk, fq[ks]);
-            }
-            if constexpr (DK)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                Frag<E> fv;
-                ld_row(fv, sV, 16 * kt + l16, 32 * ks + 8 * g);
-                acc2 = mma(acc2, fv, fx[ks]);
-              }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 16 * kt + 4 * g + i;
-              const bool on = REV ? (k >= q && k < nv) : k <= q;
-              const double gd = REV ? gs[k] - gq : gq - gs[k];
-              const float x = on ? acc[i] * exp2_fast((float)gd) : 0.f;
-              if constexpr (DK) {
-                const float f = (on && k != q) ? x * acc2[i] : 0.f;
-                rsum[i] = f;
-                csum += f;
-              }
-              acc[i] = x;
-            }
-          }
-          store_row4(sP + pair_at<E, C>(q, 16 * kt + 4 * g), acc);
-        }
-        if constexpr (DK) {
-          // over the 16 queries of the tile
-#pragma unroll
-          for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rsum[i] += __shfl_xor(rsum[i], m);
-          if (l16 == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sRR[(b * 4 + wv) * C + 16 * kt + 4 * g + i] = rsum[i];
-          }
-        }
-      }
-      if constexpr (DK) {
-        csum += __shfl_xor(csum, 16);
-        csum += __shfl_xor(csum, 32);
-        if (g == 0) sRC[(b * 2 + (NT == 2 ? (wv & 1) : 0)) * C + q] = csum;
-        if constexpr (NT == 2) {
-          // the key tile this wave has no products with
-          if (lane < 16) sRR[(b * 4 + wv) * C + 16 * (1 - (wv & 1)) + lane] = 0.f;
-        }
-      }
-      __syncthreads();  // pair matrix
-    }
-
-    // ---- 2: outputs (transposed: lane = token, four consecutive value columns) ----
-    Frag<E> fv[CT][KT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) ld_col(fv[c][kt], sV, 32 * kt + 8 * g, col0 + 16 * c, l16);
-    if constexpr (OUT) {
+      // outputs (transposed: lane = token, four consecutive value columns)
       f32x4 accO[CT][NT];
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -586,8 +648,8 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
           Frag<E> fq;
-          ld_frag_pair(fq, sQ + tile_at<E>(16 * rt + l16, 32 * ks + 4 * g),
-                       sQ + tile_at<E>(16 * rt + l16, 32 * ks + 16 + 4 * g));
+          ld_frag_pair(fq, sQ + tile_at<E, D>(16 * rt + l16, 32 * ks + 4 * g),
+                       sQ + tile_at<E, D>(16 * rt + l16, 32 * ks + 16 + 4 * g));
 #pragma unroll
           for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -603,7 +665,7 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
           accO[c][rt] *= f;
           if constexpr (DG) {
             Frag16<E> fx;
-            ld_frag16(fx, sX + tile_at<E>(16 * rt + l16, col0 + 16 * c + 4 * g));
+            ld_frag16(fx, sX + tile_at<E, D>(16 * rt + l16, col0 + 16 * c + 4 * g));
             const f32x4 x = frag16_to_f32(fx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot += x[i] * accO[c][rt][i];
@@ -616,15 +678,12 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
         }
       }
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt)
+      for (int rt = 0; rt < NT; ++rt) {
+        TF fp;
+        ld_pair(fp, sP, 16 * rt + l16, g);
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          if (REV ? kt < rt / 2 : kt > rt / 2) continue;
-          Frag<E> fp;
-          ld_pair<C>(fp, sP, 16 * rt + l16, 32 * kt + 8 * g);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) accO[c][rt] = mma(accO[c][rt], fv[c][kt], fp);
-        }
+        for (int c = 0; c < CT; ++c) accO[c][rt] = mma_tok(accO[c][rt], fv[c], fp);
+      }
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) {
         if (16 * rt + l16 >= nv) continue;
@@ -637,36 +696,40 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
       }
     }
 
-    // ---- 3: state ----
+    // state
     const float gam = sGam[b];
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt) accS[c][rt] *= gam;
+    TF fw[CT][NSV];
+    {
+      float w[TN];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(sWgt + b * C + 32 * kt + 8 * g);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(sWgt + b * C + 32 * kt + 8 * g + 4);
-      Frag<E> fw[CT][NSV];
+      for (int i = 0; i < TN; i += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i + j] = y[j];
+      }
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        float x[8];
+        float x[TN];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = frag_get(fv[c][kt], i) * (i < 4 ? w0[i & 3] : w1[i & 3]);
+        for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
         split<NSV>(fw[c], x);
       }
+    }
 #pragma unroll
-      for (int rt = 0; rt < 8; ++rt) {
-        Frag<E> fk;
-        ld_col(fk, sK, 32 * kt + 8 * g, 16 * rt, l16);
+    for (int rt = 0; rt < 8; ++rt) {
+      TF fk;
+      ld_col<D>(fk, sK, 16 * rt, l16, g);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+      for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int s = 0; s < NSV; ++s) accS[c][rt] = mma(accS[c][rt], fk, fw[c][s]);
-      }
+        for (int s = 0; s < NSV; ++s) accS[c][rt] = mma_tok(accS[c][rt], fk, fw[c][s]);
     }
   }
-  if constexpr (DG) __syncthreads();  // the last chunk's sums
+  if constexpr (DG) chunk_barrier();  // the last chunk's sums
   if (OUT) {
     if (p.fin && (REV ? first : last)) store_state(p.fin + nh * kState, accS);
     if constexpr (DG && !REV)
@@ -679,7 +742,7 @@ __global__ __launch_bounds__(320) void linear_walk_kernel(const LinearWalkArgs p
 
 template <typename E, int CT, bool REV, bool TR, bool OUT, bool DG>
 hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
-  using L = WalkLayout<E, DG ? 1 : 0>;
+  using L = WalkLayout<E, CT, DG>;
   constexpr int CB = 2 / CT;
   const int64_t blocks = (a.units + 7) / 8 * 8 * CB;
   static std::atomic<bool> set[64];
@@ -692,7 +755,7 @@ hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL((linear_walk_kernel<E, CT, REV, TR, OUT, DG>), dim3((unsigned)blocks), dim3(320), L::BYTES, stream, a);
+  hipLaunchKernelGGL((linear_walk_kernel<E, CT, REV, TR, OUT, DG>), dim3((unsigned)blocks), dim3(512), L::BYTES, stream, a);
   return hipGetLastError();
 }
 

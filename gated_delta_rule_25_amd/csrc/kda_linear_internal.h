@@ -7,8 +7,8 @@
 
 namespace kda {
 
-// Tokens per chunk: one chunk's query, key and value tiles are 16 KiB each.
-constexpr int linear_chunk_len(bool bf16) { return bf16 ? 64 : 32; }
+// Tokens per chunk: one chunk's query or key tile is 8 KiB.
+constexpr int linear_chunk_len(bool bf16) { return bf16 ? 32 : 16; }
 
 // Segments.  Every sequence is cut into segments of `seg` tokens (a multiple
 // of 64) counted from its own start; segment j of sequence n has the slot
