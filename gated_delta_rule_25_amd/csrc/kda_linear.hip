@@ -87,22 +87,53 @@ __device__ __forceinline__ int64_t slot_of(int n, int64_t bos, int seg, int64_t 
 
 // ---- LDS tiles ------------------------------------------------------------
 // A tile holds C tokens x W channels, row-major, its 16-byte units XOR-ed
-// with the row so that the 16 rows a matrix-core operand reads at one channel
-// fall on different banks.
+// with a function of the row so that what one instruction reads falls on
+// different banks.  In bytes, element (row, ch) is at
+//   row W ES + ((ch ES) ^ 16 swizzle(row)),
+// so with the lane's part of ch in an offset `at`, the rest of ch (which has
+// no bit in common with it) is one more XOR on the address, and 16 more rows
+// are an addition.
+//
+// bf16: 16 rows read at one channel need 16 different units; a transposing
+// read takes two neighbouring units of the rows 8 g .. 8 g + 3 (half a wave:
+// two g), so the upper bits of the swizzle have to tell those eight rows
+// apart: row bits 3, 1, 0 above bit 2.  Rows of half a tile (128 bytes, two to
+// a turn of the banks) leave bit 0 out.  fp32: 16 lanes of a column read take
+// four neighbouring units, and half a wave two rows that differ in bit 2:
+// the row itself.
 template <typename E, int W>
-__device__ __forceinline__ int tile_at(int row, int ch) {
-  constexpr int U = 16 / (int)sizeof(E);                  // elements per unit
-  constexpr int M = (W / U < 16 ? W / U : 16) - 1;
-  return row * W + (((ch / U) ^ (row & M)) * U) + (ch % U);
+__device__ __forceinline__ int swizzle(int row) {
+  if constexpr (sizeof(E) == 4) return row & 15;
+  else if constexpr (W == D) return (row & 8) | ((row & 3) << 1) | ((row >> 2) & 1);
+  else return ((row >> 1) & 4) | (row & 2) | ((row >> 2) & 1);
+}
+template <typename E, int W>
+__device__ __forceinline__ uint32_t tile_at(int row, int ch) {
+  return (uint32_t)(row * W * (int)sizeof(E) + ((ch * (int)sizeof(E)) ^ (swizzle<E, W>(row) << 4)));
+}
+template <typename T>
+__device__ __forceinline__ T lds_get(const unsigned char* smem, uint32_t at) {
+  return *reinterpret_cast<const T*>(smem + at);
 }
 
-// operand with the channels ch .. ch+7 of a row
-__device__ __forceinline__ void ld_row(Frag<__bf16>& f, const __bf16* t, int row, int ch) {
-  f.v = *reinterpret_cast<const bf16x8*>(t + tile_at<__bf16, D>(row, ch));
+// operand with the channels ch .. ch+7 of a row; `at` = the lane's 8 g, ch0 = 32 ks
+__device__ __forceinline__ void ld_row(Frag<__bf16>& f, const unsigned char* m, uint32_t at, int ch0) {
+  f.v = lds_get<bf16x8>(m, at ^ (uint32_t)(ch0 * 2));
 }
-__device__ __forceinline__ void ld_row(Frag<float>& f, const float* t, int row, int ch) {
-  f.lo = *reinterpret_cast<const f32x4*>(t + tile_at<float, D>(row, ch));
-  f.hi = *reinterpret_cast<const f32x4*>(t + tile_at<float, D>(row, ch + 4));
+__device__ __forceinline__ void ld_row(Frag<float>& f, const unsigned char* m, uint32_t at, int ch0) {
+  f.lo = lds_get<f32x4>(m, at ^ (uint32_t)(ch0 * 4));
+  f.hi = lds_get<f32x4>(m, at ^ (uint32_t)(ch0 * 4 + 16));
+}
+// operand with the channels ch0 + 4 g .. and ch0 + 16 + 4 g .. of a row (what
+// two stacked accumulator tiles hold); `at` = the lane's 4 g
+__device__ __forceinline__ void ld_row_acc(Frag<__bf16>& f, const unsigned char* m, uint32_t at, int ch0, int rows) {
+  const bf16x4 a = lds_get<bf16x4>(m, (at ^ (uint32_t)(ch0 * 2)) + rows * (D * 2));
+  const bf16x4 b = lds_get<bf16x4>(m, (at ^ (uint32_t)(ch0 * 2 + 32)) + rows * (D * 2));
+  f.v = (bf16x8){a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ void ld_row_acc(Frag<float>& f, const unsigned char* m, uint32_t at, int ch0, int rows) {
+  f.lo = lds_get<f32x4>(m, (at ^ (uint32_t)(ch0 * 4)) + rows * (D * 4));
+  f.hi = lds_get<f32x4>(m, (at ^ (uint32_t)(ch0 * 4 + 64)) + rows * (D * 4));
 }
 
 // Operands whose contraction runs over a chunk's tokens: 32 deep in bf16
@@ -112,12 +143,14 @@ struct Tok;
 template <>
 struct Tok<__bf16> {
   using F = Frag<__bf16>;
-  static constexpr int N = 8;
+  static constexpr int N = 8;      // tokens a lane holds
+  static constexpr int READS = 2;  // LDS reads of a column
 };
 template <>
 struct Tok<float> {
   using F = Frag16<float>;
   static constexpr int N = 4;
+  static constexpr int READS = 4;
 };
 __device__ __forceinline__ f32x4 mma_tok(f32x4 acc, const Frag<__bf16>& a, const Frag<__bf16>& b) {
   return mma(acc, a, b);
@@ -125,45 +158,64 @@ __device__ __forceinline__ f32x4 mma_tok(f32x4 acc, const Frag<__bf16>& a, const
 __device__ __forceinline__ f32x4 mma_tok(f32x4 acc, const Frag16<float>& a, const Frag16<float>& b) {
   return mma16(acc, a, b);
 }
-// column ch0 + l16 over the lane's tokens.  bf16: the transposing LDS read
-// hands each lane of 16 one column of a 4-row x 16-channel block, whose rows
-// the lanes 4r .. 4r+3 address.
+// A column over the lane's tokens.  bf16: the transposing LDS read hands each
+// lane of 16 one column of a 4-row x 16-channel block, whose rows the lanes
+// 4r .. 4r+3 address.  col_at: the lane's offsets (two reads in bf16, four in
+// fp32) at column 0 of a tile; ch0 is a multiple of 16.
 template <int W>
-__device__ __forceinline__ void ld_col(Frag<__bf16>& f, const __bf16* t, int ch0, int l16, int g) {
+__device__ __forceinline__ void col_at(uint32_t (&at)[2], const __bf16*, int ch, int l16, int g) {
+  const int r = 8 * g + (l16 >> 2), c = ch + 4 * (l16 & 3);
+  at[0] = tile_at<__bf16, W>(r, c);
+  at[1] = tile_at<__bf16, W>(r + 4, c);
+}
+template <int W>
+__device__ __forceinline__ void col_at(uint32_t (&at)[4], const float*, int ch, int l16, int g) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at[i] = tile_at<float, W>(4 * g + i, ch + l16);
+}
+__device__ __forceinline__ void ld_col(Frag<__bf16>& f, unsigned char* m, uint32_t base, const uint32_t (&at)[2], int ch0) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const int r = 8 * g + (l16 >> 2), c = ch0 + 4 * (l16 & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16, W>(r, c)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + tile_at<__bf16, W>(r + 4, c)));
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(m + ((base + at[0]) ^ (uint32_t)(ch0 * 2))));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(m + ((base + at[1]) ^ (uint32_t)(ch0 * 2))));
   const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
   f.v = (bf16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 }
-template <int W>
-__device__ __forceinline__ void ld_col(Frag16<float>& f, const float* t, int ch0, int l16, int g) {
+__device__ __forceinline__ void ld_col(Frag16<float>& f, unsigned char* m, uint32_t base, const uint32_t (&at)[4], int ch0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = t[tile_at<float, W>(4 * g + i, ch0 + l16)];
+  for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>(m, (base + at[i]) ^ (uint32_t)(ch0 * 4));
 }
-// a row of the pair matrix over the lane's tokens (rows of 64 bytes: a wave
-// reads 16 of them whole)
-__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const __bf16* t, int row, int g) {
-  f.v = *reinterpret_cast<const bf16x8*>(t + row * 32 + 8 * g);
-}
-__device__ __forceinline__ void ld_pair(Frag16<float>& f, const float* t, int row, int g) {
-  f.v = *reinterpret_cast<const f32x4*>(t + row * 16 + 4 * g);
-}
+// The pair matrix: rows of 64 bytes, four to a turn of the banks, their
+// 16-byte units XOR-ed with row / 4.  pair_at: the byte offset of unit u.
+__device__ __forceinline__ uint32_t pair_at(int row, int u) { return (uint32_t)(row * 64 + ((u ^ ((row >> 2) & 3)) << 4)); }
+// a row over the lane's tokens (unit g)
+__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<bf16x8>(m, at); }
+__device__ __forceinline__ void ld_pair(Frag16<float>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<f32x4>(m, at); }
 __device__ __forceinline__ float frag_get(const Frag<__bf16>& f, int i) { return (float)f.v[i]; }
 __device__ __forceinline__ float frag_get(const Frag16<float>& f, int i) { return f.v[i]; }
 
-// x as the sum of NS operands (bf16: NS terms of 8 bits each; fp32: itself).
+// x as the sum of NS operands.  bf16, one term: rounded to nearest.  Three
+// terms: the 24 significant bits cut in three (each subtraction is exact), the
+// high halves of two words packed by one byte permutation.  fp32: itself.
 template <int NS>
 __device__ __forceinline__ void split(Frag<__bf16> (&f)[NS], const float (&x)[8]) {
+  if constexpr (NS == 1) {
+    frag_from_f32(f[0], x);
+  } else {
+    static_assert(NS == 3, "one or three terms");
+    uint32_t t[3][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float r = x[i];
+    for (int i = 0; i < 8; ++i) {
+      t[0][i] = __builtin_bit_cast(uint32_t, x[i]);
+      const float r = x[i] - __builtin_bit_cast(float, t[0][i] & 0xffff0000u);
+      t[1][i] = __builtin_bit_cast(uint32_t, r);
+      t[2][i] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, t[1][i] & 0xffff0000u));
+    }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const __bf16 b = (__bf16)r;
-      f[s].v[i] = b;
-      r -= (float)b;
+    for (int s = 0; s < 3; ++s) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(t[s][2 * i + 1], t[s][2 * i], 0x07060302u);
+      f[s].v = __builtin_bit_cast(bf16x8, w);
     }
   }
 }
@@ -185,6 +237,47 @@ __device__ __forceinline__ void chunk_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Moves of a double between the lanes of a row of 16, without LDS: lane l
+// gets lane l - N (shr) or l + N (shl), zero where there is none.
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double read_lane(double x, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sums over the lanes 0 .. lane (prefix) and lane .. C - 1 (suffix) of C = 16 or 32 lanes.
+template <int C>
+__device__ __forceinline__ double prefix_sum(double x, int lane) {
+  x += dpp_move<0x111>(x);
+  x += dpp_move<0x112>(x);
+  x += dpp_move<0x114>(x);
+  x += dpp_move<0x118>(x);
+  if constexpr (C == 32) {
+    const double low = read_lane(x, 15);
+    if (lane >= 16) x += low;
+  }
+  return x;
+}
+template <int C>
+__device__ __forceinline__ double suffix_sum(double x, int lane) {
+  x += dpp_move<0x101>(x);
+  x += dpp_move<0x102>(x);
+  x += dpp_move<0x104>(x);
+  x += dpp_move<0x108>(x);
+  if constexpr (C == 32) {
+    const double high = read_lane(x, 16);
+    if (lane < 16) x += high;
+  }
+  return x;
 }
 
 template <typename E, int CT, bool DG>
@@ -313,14 +406,13 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
       constexpr int NPC = C * W * ES / 1024;   // pieces
       constexpr int UR = W * ES / 16;          // 16-byte units per row
       constexpr int RP = 64 / UR;              // rows per piece
-      constexpr int M = (UR < 16 ? UR : 16) - 1;
       const uint32_t stride = (uint32_t)heads * (D * ES);
       const char* base = static_cast<const char*>(src) + ((size_t)t0 * heads + h / (H / heads)) * (D * ES);
       const Rsrc rs = make_rsrc(base, (uint32_t)(nv - 1) * stride + D * ES);
       uint32_t row = (uint32_t)(lane / UR) * stride + ch0 * ES;
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
-        const uint32_t unit = (uint32_t)(((lane % UR) ^ ((i * RP + lane / UR) & M)) * 16);
+        const uint32_t unit = (uint32_t)(((lane % UR) ^ swizzle<E, W>(i * RP + lane / UR)) * 16);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + i * 1024), 16,
                                                  (int)(row + unit), 0, 0, 0);
         row += RP * stride;
@@ -352,21 +444,23 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
 
   if (wv == 6) {
     // ---- decays ----
+    // rows behind the end lie outside the buffer view and read zero
+    auto load_rows = [&](const float* src, int ci) -> float {
+      const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+      const int nv = (int)min((int64_t)C, te - t0);
+      const Rsrc rs = make_rsrc(src + (size_t)t0 * H + h, ci >= 0 && ci < nch ? (uint32_t)((nv - 1) * H + 1) * 4 : 0);
+      return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, lane < C ? lane * H * 4 : -4, 0, 0));
+    };
+    const float la_head = p.decay_per_head ? p.log_decay[h] : 0.f;
     auto load_decay = [&](int ci) -> float {
-      const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
-      if (ci >= nch || lane >= C || t >= te) return 0.f;
-      return p.decay_per_head ? p.log_decay[h] : p.log_decay[(size_t)t * H + h];
+      if (!p.decay_per_head) return load_rows(p.log_decay, ci);
+      return lane < C && tb + (int64_t)chunk_of(ci) * C + lane < te ? la_head : 0.f;
     };
     double log_total = 0.0;
     auto put_decay = [&](int ci, float la) {
       const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
-      double s = (double)fmaxf(la, kMinLogDecay) * kLog2e;
-#pragma unroll
-      for (int m = 1; m < C; m <<= 1) {
-        const double o = __shfl_up(s, m);
-        if (lane >= m) s += o;
-      }
-      const double tot = __shfl(s, C - 1);
+      const double s = prefix_sum<C>((double)fmaxf(la, kMinLogDecay) * kLog2e, lane);
+      const double tot = read_lane(s, C - 1);
       log_total += tot;
       const float head = exp2_fast((float)s), tail = exp2_fast((float)(tot - s));
       const int b = ci & 3;
@@ -402,41 +496,30 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
         const int64_t tend = min(te, t0 + C);
         if (tend == te || (tend - bos) % p.seg == 0)
           flow = (double)sAnc[b * 4] + (double)sAnc[b * 4 + 1] + (double)sAnc[b * 4 + 2] + (double)sAnc[b * 4 + 3];
-        double s = in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0;
-#pragma unroll
-        for (int m = 1; m < C; m <<= 1) {
-          const double o = __shfl_down(s, m);
-          if (lane + m < C) s += o;
-        }
+        const double s = suffix_sum<C>(in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0, lane);
         const double d = flow + s;
         if (in) {
           if (p.d_log_decay) p.d_log_decay[(size_t)(t0 + lane) * H + h] = (float)d;
           dsum += d;
         }
-        flow += __shfl(s, 0);
+        flow += read_lane(s, 0);
       }
-    };
-    auto load_rdot = [&](int ci) -> float {
-      if constexpr (DK) {
-        const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
-        if (ci >= 0 && lane < C && t < te) return p.row_dot[(size_t)t * H + h];
-      }
-      return 0.f;
     };
     if (nch > 0) put_decay(0, load_decay(0));
-    float la = load_decay(1), rdot = 0.f;
+    // two iterations ahead of their use, one in flight over a barrier
+    float la_next = load_decay(1), rdot_next = 0.f;
     for (int ci = -1; ci < nch; ++ci) {
       chunk_barrier();
-      const float la_next = load_decay(ci + 3), rdot_next = load_rdot(ci);
+      const float la = la_next, rdot = rdot_next;
+      la_next = load_decay(ci + 3);
+      if constexpr (DK) rdot_next = load_rows(p.row_dot, ci);
       if (ci + 2 < nch) put_decay(ci + 2, la);
       if constexpr (DG)
         if (ci > 0) finish(ci - 1, rdot);
-      la = la_next;
-      rdot = rdot_next;
     }
     if constexpr (DG) {
       chunk_barrier();
-      if (nch > 0) finish(nch - 1, rdot);
+      if (nch > 0) finish(nch - 1, rdot_next);
       if constexpr (REV) {
         if (p.d_decay_part) {
 #pragma unroll
@@ -453,25 +536,22 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     // ---- pair matrix of chunk ci + 1, keys in rows: lane = query, four consecutive keys ----
     const int rt = wv - 4;
     const int q = 16 * rt + l16;
+    const uint32_t q_at = tile_at<E, D>(q, 8 * g), k_at = tile_at<E, D>(l16, 8 * g);
     for (int ci = -1; ci < nch; ++ci) {
       chunk_barrier();
       if (!OUT || rt >= NT || ci + 1 >= nch) continue;
-      const unsigned char* buf = tiles(ci + 1);
-      const E* sQ = reinterpret_cast<const E*>(buf);
-      const E* sK = reinterpret_cast<const E*>(buf + L::K);
-      const E* sV = reinterpret_cast<const E*>(buf + L::V);
-      const E* sX = reinterpret_cast<const E*>(buf + L::X);
-      E* sP = reinterpret_cast<E*>(smem + L::PAIR) + ((ci + 1) & 1) * (C * C);
+      const uint32_t base = (uint32_t)((ci + 1) % NBUF) * L::SET;
+      unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * C * ES);
       const int b = (ci + 1) & 3;
       const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
       const int nv = (int)min((int64_t)C, te - t0);
       Frag<E> fq[4];
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], sQ, q, 32 * ks + 8 * g);
+      for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], smem, base + q_at, 32 * ks);
       Frag<E> fx[DK ? 4 : 1];
       if constexpr (DK)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], sX, q, 32 * ks + 8 * g);
+        for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], smem, base + L::X + q_at, 32 * ks);
       const float* gs = sSum + b * 2 * C;
       const float gq = gs[q], gq_lo = gs[C + q];
       float csum = 0.f;
@@ -484,14 +564,14 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             Frag<E> fk;
-            ld_row(fk, sK, 16 * kt + l16, 32 * ks + 8 * g);
+            ld_row(fk, smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
             acc = mma(acc, fk, fq[ks]);
           }
           if constexpr (DK)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               Frag<E> fv;
-              ld_row(fv, sV, 16 * kt + l16, 32 * ks + 8 * g);
+              ld_row(fv, smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
               acc2 = mma(acc2, fv, fx[ks]);
             }
           const f32x4 gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
@@ -511,7 +591,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
             acc[i] = x;
           }
         }
-        store_row4(sP + q * C + 16 * kt + 4 * g, acc);
+        store_row4(reinterpret_cast<E*>(pair + (BF ? pair_at(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at(q, g))), acc);
         if constexpr (DK) {
           // over the 16 queries of the tile
 #pragma unroll
@@ -583,17 +663,21 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
         for (int rt = 0; rt < 8; ++rt) accS[c][rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
   }
+  // lane offsets within the tiles and the output rows
+  uint32_t k_at[Tok<E>::READS], v_at[Tok<E>::READS];
+  col_at<D>(k_at, static_cast<const E*>(nullptr), 0, l16, g);
+  col_at<L::VW>(v_at, static_cast<const E*>(nullptr), vc0, l16, g);
+  const uint32_t q_at = tile_at<E, D>(l16, 4 * g), x_at = tile_at<E, D>(l16, col0 + 4 * g);
+  const uint32_t p_at = pair_at(l16, g);
+  const int oes = TR && p.o_f32 ? 4 : ES;
+  const uint32_t o_row = (uint32_t)H * (D * oes);
+  const uint32_t o_at = (uint32_t)l16 * o_row + (uint32_t)((col0 + 4 * g) * oes);
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
+  uint32_t base = 0;  // of the chunk's tiles
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
-    const unsigned char* buf = tiles(ci);
-    const E* sQ = reinterpret_cast<const E*>(buf);
-    const E* sK = reinterpret_cast<const E*>(buf + L::K);
-    const E* sV = reinterpret_cast<const E*>(buf + L::V);
-    const E* sX = reinterpret_cast<const E*>(buf + L::X);
-    const E* sP = reinterpret_cast<const E*>(smem + L::PAIR) + (ci & 1) * (C * C);
     const int b = ci & 3;
 
     // what the decays' gradient needs of the states at segment boundaries
@@ -622,11 +706,38 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     }
     chunk_barrier();
 
-    TF fv[CT];
+    // The LDS reads run a few operands ahead of the products, in the order of
+    // use: at most 15 can be waited for one by one.
+    TF fv[CT], fk[8];
+    float w[TN], gam = 0.f;
+    auto read_v = [&]() {
 #pragma unroll
-    for (int c = 0; c < CT; ++c) ld_col<L::VW>(fv[c], sV, vc0 + 16 * c, l16, g);
+      for (int c = 0; c < CT; ++c) ld_col(fv[c], smem, base + L::V, v_at, 16 * c);
+    };
+    auto read_w = [&]() {
+#pragma unroll
+      for (int i = 0; i < TN; i += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i + j] = y[j];
+      }
+      gam = sGam[b];
+    };
+    auto read_k = [&](int first, int count) {
+#pragma unroll
+      for (int rt = 0; rt < 8; ++rt)
+        if (rt >= first && rt < first + count) ld_col(fk[rt], smem, base + L::K, k_at, 16 * rt);
+    };
     if constexpr (OUT) {
       // outputs (transposed: lane = token, four consecutive value columns)
+      Frag<E> fq[4][NT];
+      TF fp[NT];
+      float row[NT];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks][rt], smem, base + q_at, 32 * ks, 16 * rt);
+      __builtin_amdgcn_sched_barrier(0);
       f32x4 accO[CT][NT];
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -646,26 +757,34 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
           split<NSS>(fs[c], x);
         }
 #pragma unroll
-        for (int rt = 0; rt < NT; ++rt) {
-          Frag<E> fq;
-          ld_frag_pair(fq, sQ + tile_at<E, D>(16 * rt + l16, 32 * ks + 4 * g),
-                       sQ + tile_at<E, D>(16 * rt + l16, 32 * ks + 16 + 4 * g));
+        for (int s = 0; s < NSS; ++s)
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+          for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-            for (int s = 0; s < NSS; ++s) accO[c][rt] = mma(accO[c][rt], fs[c][s], fq);
+            for (int c = 0; c < CT; ++c) accO[c][rt] = mma(accO[c][rt], fs[c][s], fq[ks][rt]);
+        if (ks == 0) {
+#pragma unroll
+          for (int rt = 0; rt < NT; ++rt) row[rt] = sRow[b * C + 16 * rt + l16];
+          read_v();
+        } else if (ks == 1) {
+#pragma unroll
+          for (int rt = 0; rt < NT; ++rt)
+            ld_pair(fp[rt], smem, L::PAIR + (ci & 1) * (C * C * ES) + p_at + 16 * rt * 64);
+          read_w();
+        } else {
+          read_k(2 * (ks - 2), 2);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) {
-        const float f = sRow[b * C + 16 * rt + l16];
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          accO[c][rt] *= f;
+          accO[c][rt] *= row[rt];
           if constexpr (DG) {
             Frag16<E> fx;
-            ld_frag16(fx, sX + tile_at<E, D>(16 * rt + l16, col0 + 16 * c + 4 * g));
+            ld_frag16(fx, reinterpret_cast<const E*>(smem + ((base + L::X + x_at) ^ (uint32_t)(16 * c * ES)) + 16 * rt * (D * ES)));
             const f32x4 x = frag16_to_f32(fx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot += x[i] * accO[c][rt][i];
@@ -678,56 +797,54 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
         }
       }
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        TF fp;
-        ld_pair(fp, sP, 16 * rt + l16, g);
+      for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) accO[c][rt] = mma_tok(accO[c][rt], fv[c], fp);
-      }
+        for (int c = 0; c < CT; ++c) accO[c][rt] = mma_tok(accO[c][rt], fv[c], fp[rt]);
+      read_k(4, 4);
+      __builtin_amdgcn_sched_barrier(0);
+      // rows behind the end fall outside the buffer view and are dropped
+      const Rsrc orb = make_rsrc(static_cast<char*>(p.o) + ((size_t)t0 * H + h) * (D * oes),
+                                 (uint32_t)(nv - 1) * o_row + D * oes);
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        if (16 * rt + l16 >= nv) continue;
-        const size_t at = ((size_t)(t0 + 16 * rt + l16) * H + h) * D + col0 + 4 * g;
+      for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          if (p.o_f32) store_row4(static_cast<float*>(p.o) + at + 16 * c, accO[c][rt]);
-          else store_row4(static_cast<E*>(p.o) + at + 16 * c, accO[c][rt]);
+          const int off = (int)(o_at + 16 * rt * o_row + 16 * c * oes);
+          if (!BF || (TR && p.o_f32)) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, accO[c][rt]), orb, off, 0, 0);
+          } else {
+            const f32x4 t = accO[c][rt];
+            const bf16x4 y = (bf16x4){(__bf16)t[0], (__bf16)t[1], (__bf16)t[2], (__bf16)t[3]};
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), orb, off, 0, 0);
+          }
         }
-      }
     }
 
     // state
-    const float gam = sGam[b];
+    if constexpr (!OUT) {
+      read_v();
+      read_w();
+      read_k(0, 8);
+    }
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt) accS[c][rt] *= gam;
     TF fw[CT][NSV];
-    {
-      float w[TN];
 #pragma unroll
-      for (int i = 0; i < TN; i += 4) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
+    for (int c = 0; c < CT; ++c) {
+      float x[TN];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[i + j] = y[j];
-      }
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        float x[TN];
-#pragma unroll
-        for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
-        split<NSV>(fw[c], x);
-      }
+      for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
+      split<NSV>(fw[c], x);
     }
 #pragma unroll
-    for (int rt = 0; rt < 8; ++rt) {
-      TF fk;
-      ld_col<D>(fk, sK, 16 * rt, l16, g);
+    for (int s = 0; s < NSV; ++s)
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
+      for (int rt = 0; rt < 8; ++rt)
 #pragma unroll
-        for (int s = 0; s < NSV; ++s) accS[c][rt] = mma_tok(accS[c][rt], fk, fw[c][s]);
-    }
+        for (int c = 0; c < CT; ++c) accS[c][rt] = mma_tok(accS[c][rt], fk[rt], fw[c][s]);
+    base = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
   }
   if constexpr (DG) chunk_barrier();  // the last chunk's sums
   if (OUT) {
