@@ -94,17 +94,21 @@ __device__ __forceinline__ int64_t slot_of(int n, int64_t bos, int seg, int64_t 
 // no bit in common with it) is one more XOR on the address, and 16 more rows
 // are an addition.
 //
-// bf16: 16 rows read at one channel need 16 different units; a transposing
-// read takes two neighbouring units of the rows 8 g .. 8 g + 3 (half a wave:
-// two g), so the upper bits of the swizzle have to tell those eight rows
-// apart: row bits 3, 1, 0 above bit 2.  Rows of half a tile (128 bytes, two to
-// a turn of the banks) leave bit 0 out.  fp32: 16 lanes of a column read take
-// four neighbouring units, and half a wave two rows that differ in bit 2:
-// the row itself.
+// What one LDS cycle serves (measured with the conflict counter): 32
+// consecutive lanes of an 8-byte read, the lanes 0-3, 12-15, 20-27 (and so on)
+// of a 16-byte read.  bf16, rows of 256 bytes: 16 rows read at one channel
+// need 16 different units; a transposing read takes two neighbouring units of
+// the rows 8 g .. 8 g + 3 for two g, so the upper three bits of the swizzle
+// have to tell those eight rows apart; a 16-byte read takes unit u of the rows
+// 0-3, 12-15 and unit u ^ 1 of the rows 4-11, so each of these two sets has to
+// fill whole pairs of units.  Rows of half a tile (128 bytes, two to a turn of
+// the banks) are only read transposing.  fp32: 16 lanes of a column read take
+// four neighbouring units, and half a wave two rows that differ in bit 2: the
+// row itself.
 template <typename E, int W>
 __device__ __forceinline__ int swizzle(int row) {
   if constexpr (sizeof(E) == 4) return row & 15;
-  else if constexpr (W == D) return (row & 8) | ((row & 3) << 1) | ((row >> 2) & 1);
+  else if constexpr (W == D) return ((row ^ (row << 1)) & 8) | ((row & 3) << 1) | ((row >> 2) & 1);
   else return ((row >> 1) & 4) | (row & 2) | ((row >> 2) & 1);
 }
 template <typename E, int W>
@@ -184,9 +188,13 @@ __device__ __forceinline__ void ld_col(Frag16<float>& f, unsigned char* m, uint3
 #pragma unroll
   for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>(m, (base + at[i]) ^ (uint32_t)(ch0 * 4));
 }
-// The pair matrix: rows of 64 bytes, four to a turn of the banks, their
-// 16-byte units XOR-ed with row / 4.  pair_at: the byte offset of unit u.
-__device__ __forceinline__ uint32_t pair_at(int row, int u) { return (uint32_t)(row * 64 + ((u ^ ((row >> 2) & 3)) << 4)); }
+// The pair matrix: rows of 64 bytes, four to a turn of the banks; the 16-byte
+// units XOR-ed so that the rows of a quarter read (above) fall on all banks.
+// pair_at: the byte offset of unit u.
+__device__ __forceinline__ uint32_t pair_at(int row, int u) {
+  const int hi = (row >> 3) & 1, lo = (row >> 2) & 1;
+  return (uint32_t)(row * 64 + ((u ^ ((hi ^ lo) << 1 | hi)) << 4));
+}
 // a row over the lane's tokens (unit g)
 __device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<bf16x8>(m, at); }
 __device__ __forceinline__ void ld_pair(Frag16<float>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<f32x4>(m, at); }
@@ -672,9 +680,17 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   const int oes = TR && p.o_f32 ? 4 : ES;
   const uint32_t o_row = (uint32_t)H * (D * oes);
   const uint32_t o_at = (uint32_t)l16 * o_row + (uint32_t)((col0 + 4 * g) * oes);
+  Frag<E> fq[OUT ? 4 : 1][NT];
+  auto read_q = [&](uint32_t at) {
+#pragma unroll
+    for (int ks = 0; ks < (OUT ? 4 : 0); ++ks)
+#pragma unroll
+      for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks][rt], smem, at + q_at, 32 * ks, 16 * rt);
+  };
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
   uint32_t base = 0;  // of the chunk's tiles
+  read_q(base);
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
@@ -707,38 +723,50 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     chunk_barrier();
 
     // The LDS reads run a few operands ahead of the products, in the order of
-    // use: at most 15 can be waited for one by one.
+    // use (at most 15 can be waited for one by one); the vector arithmetic
+    // fills the gaps between products.
+    const uint32_t base_next = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
+    const float gam = sGam[b];
+    float w[TN];
+#pragma unroll
+    for (int i = 0; i < TN; i += 4) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i + j] = y[j];
+    }
     TF fv[CT], fk[8];
-    float w[TN], gam = 0.f;
-    auto read_v = [&]() {
 #pragma unroll
-      for (int c = 0; c < CT; ++c) ld_col(fv[c], smem, base + L::V, v_at, 16 * c);
-    };
-    auto read_w = [&]() {
-#pragma unroll
-      for (int i = 0; i < TN; i += 4) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[i + j] = y[j];
-      }
-      gam = sGam[b];
-    };
+    for (int c = 0; c < CT; ++c) ld_col(fv[c], smem, base + L::V, v_at, 16 * c);
     auto read_k = [&](int first, int count) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt)
         if (rt >= first && rt < first + count) ld_col(fk[rt], smem, base + L::K, k_at, 16 * rt);
     };
+    auto decay_state = [&](int rt) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) accS[c][rt] *= gam;
+    };
+    // values times their factors, in the terms of the state's update
+    TF fw[CT][NSV];
+    auto weigh_values = [&]() {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float x[TN];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
+        split<NSV>(fw[c], x);
+      }
+    };
+    f32x4 accO[OUT ? CT : 1][NT];
     if constexpr (OUT) {
       // outputs (transposed: lane = token, four consecutive value columns)
-      Frag<E> fq[4][NT];
       TF fp[NT];
       float row[NT];
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
+      for (int rt = 0; rt < NT; ++rt) row[rt] = sRow[b * C + 16 * rt + l16];
 #pragma unroll
-        for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks][rt], smem, base + q_at, 32 * ks, 16 * rt);
-      __builtin_amdgcn_sched_barrier(0);
-      f32x4 accO[CT][NT];
+      for (int rt = 0; rt < NT; ++rt)
+        ld_pair(fp[rt], smem, L::PAIR + (ci & 1) * (C * C * ES) + p_at + 16 * rt * 64);
 #pragma unroll
       for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -762,20 +790,14 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
           for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int c = 0; c < CT; ++c) accO[c][rt] = mma(accO[c][rt], fs[c][s], fq[ks][rt]);
-        if (ks == 0) {
-#pragma unroll
-          for (int rt = 0; rt < NT; ++rt) row[rt] = sRow[b * C + 16 * rt + l16];
-          read_v();
-        } else if (ks == 1) {
-#pragma unroll
-          for (int rt = 0; rt < NT; ++rt)
-            ld_pair(fp[rt], smem, L::PAIR + (ci & 1) * (C * C * ES) + p_at + 16 * rt * 64);
-          read_w();
-        } else {
-          read_k(2 * (ks - 2), 2);
-        }
+        decay_state(2 * ks);
+        decay_state(2 * ks + 1);
+        if (ks >= 2) read_k(2 * (ks - 2), 2);
         __builtin_amdgcn_sched_barrier(0);
       }
+      weigh_values();
+      read_k(4, 4);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) {
         float dot = 0.f;
@@ -800,8 +822,23 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
       for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
         for (int c = 0; c < CT; ++c) accO[c][rt] = mma_tok(accO[c][rt], fv[c], fp[rt]);
-      read_k(4, 4);
-      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      read_k(0, 8);
+#pragma unroll
+      for (int rt = 0; rt < 8; ++rt) decay_state(rt);
+      weigh_values();
+    }
+    // state, with the outputs' stores in between
+#pragma unroll
+    for (int s = 0; s < NSV; ++s)
+#pragma unroll
+      for (int rt = 0; rt < 8; ++rt)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) accS[c][rt] = mma_tok(accS[c][rt], fk[rt], fw[c][s]);
+    if constexpr (OUT) {
+      // the next chunk's queries: its tiles are in LDS already (the last chunk
+      // reads what is there and drops it)
+      read_q(base_next);
       // rows behind the end fall outside the buffer view and are dropped
       const Rsrc orb = make_rsrc(static_cast<char*>(p.o) + ((size_t)t0 * H + h) * (D * oes),
                                  (uint32_t)(nv - 1) * o_row + D * oes);
@@ -819,32 +856,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
           }
         }
     }
-
-    // state
-    if constexpr (!OUT) {
-      read_v();
-      read_w();
-      read_k(0, 8);
-    }
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int rt = 0; rt < 8; ++rt) accS[c][rt] *= gam;
-    TF fw[CT][NSV];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      float x[TN];
-#pragma unroll
-      for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
-      split<NSV>(fw[c], x);
-    }
-#pragma unroll
-    for (int s = 0; s < NSV; ++s)
-#pragma unroll
-      for (int rt = 0; rt < 8; ++rt)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) accS[c][rt] = mma_tok(accS[c][rt], fk[rt], fw[c][s]);
-    base = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
+    base = base_next;
   }
   if constexpr (DG) chunk_barrier();  // the last chunk's sums
   if (OUT) {
