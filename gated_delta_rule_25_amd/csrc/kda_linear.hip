@@ -188,12 +188,15 @@ __device__ __forceinline__ void ld_col(Frag16<float>& f, unsigned char* m, uint3
 #pragma unroll
   for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>(m, (base + at[i]) ^ (uint32_t)(ch0 * 4));
 }
-// The pair matrix: rows of 64 bytes, four to a turn of the banks; the 16-byte
-// units XOR-ed so that the rows of a quarter read (above) fall on all banks.
-// pair_at: the byte offset of unit u.
+// The pair matrix: rows of RB = 64 or 128 bytes, their 16-byte units XOR-ed so
+// that the rows of a 16-byte read (above) fall on all banks.  pair_at: the
+// byte offset of unit u; the tokens of step kt are the units 4 kt ...
+template <int RB>
 __device__ __forceinline__ uint32_t pair_at(int row, int u) {
-  const int hi = (row >> 3) & 1, lo = (row >> 2) & 1;
-  return (uint32_t)(row * 64 + ((u ^ ((hi ^ lo) << 1 | hi)) << 4));
+  static_assert(RB == 64 || RB == 128, "two row lengths");
+  const int b3 = (row >> 3) & 1, b2 = (row >> 2) & 1, b1 = (row >> 1) & 1;
+  const int x = RB == 64 ? (b3 ^ b2) << 1 | b3 : (b3 ^ b2) << 2 | b1 << 1 | b3;
+  return (uint32_t)(row * RB + ((u ^ x) << 4));
 }
 // a row over the lane's tokens (unit g)
 __device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<bf16x8>(m, at); }
@@ -262,18 +265,20 @@ __device__ __forceinline__ double read_lane(double x, int l) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// Sums over the lanes 0 .. lane (prefix) and lane .. C - 1 (suffix) of C = 16 or 32 lanes.
+// Sums over the lanes 0 .. lane (prefix) and lane .. C - 1 (suffix) of C lanes.
 template <int C>
 __device__ __forceinline__ double prefix_sum(double x, int lane) {
   x += dpp_move<0x111>(x);
   x += dpp_move<0x112>(x);
   x += dpp_move<0x114>(x);
   x += dpp_move<0x118>(x);
-  if constexpr (C == 32) {
-    const double low = read_lane(x, 15);
-    if (lane >= 16) x += low;
+  double low = 0.0;
+#pragma unroll
+  for (int r = 16; r < C; r += 16) {
+    const double t = read_lane(x, r - 1);
+    low += lane >= r ? t : 0.0;
   }
-  return x;
+  return x + low;
 }
 template <int C>
 __device__ __forceinline__ double suffix_sum(double x, int lane) {
@@ -281,63 +286,72 @@ __device__ __forceinline__ double suffix_sum(double x, int lane) {
   x += dpp_move<0x102>(x);
   x += dpp_move<0x104>(x);
   x += dpp_move<0x108>(x);
-  if constexpr (C == 32) {
-    const double high = read_lane(x, 16);
-    if (lane < 16) x += high;
+  double high = 0.0;
+#pragma unroll
+  for (int r = C - 16; r > 0; r -= 16) {
+    const double t = read_lane(x, r);
+    high += lane < r ? t : 0.0;
   }
-  return x;
+  return x + high;
 }
 
-template <typename E, int CT, bool DG>
+// NW compute waves of 16 value columns each: 4 (half a head) or 8 (a head).
+// Chunks of 64 tokens for half heads, 32 for whole ones (half of that in
+// fp32), so that a query or key tile is 16 or 8 KiB.
+template <typename E, int NW, bool DG>
 struct WalkLayout {
-  static constexpr int C = linear_chunk_len(sizeof(E) == 2);
   static constexpr int ES = (int)sizeof(E);
-  static constexpr int TILE = C * D * ES;              // 8 KiB: a query, key or x tile
-  static constexpr int VW = 64 * CT;                   // value columns of the workgroup
+  static constexpr int C = (NW == 4 ? 128 : 64) / ES;
+  static constexpr int TILE = C * D * ES;              // a query, key or x tile
+  static constexpr int VW = 16 * NW;                   // value columns of the workgroup
   static constexpr int VTILE = C * VW * ES;
   static constexpr int K = TILE, V = 2 * TILE, X = V + VTILE;
   static constexpr int SET = X + (DG ? TILE : 0);      // the tiles of a chunk
-  static constexpr int NBUF = DG ? 4 : CT == 2 ? 5 : 6;  // chunks in LDS
+  static constexpr int NBUF = NW == 4 ? 3 : DG ? 4 : 5;  // chunks in LDS
   static constexpr int COPIES = SET / 1024;            // copy instructions per chunk
+  static constexpr int RB = C * ES;                    // bytes of a pair matrix row
   static constexpr int PAIR = NBUF * SET;              // E [2][C][C]
-  static constexpr int SUM = PAIR + 2 * C * C * ES;    // float [4][2][C] prefix sums (log2), high and low part
+  static constexpr int SUM = PAIR + 2 * C * RB;        // float [4][2][C] prefix sums (log2), high and low part
   static constexpr int ROW = SUM + 4 * 2 * C * 4;      // float [4][C] factor of the state in row t
   static constexpr int WGT = ROW + 4 * C * 4;          // float [4][C] factor of token t in the state
   static constexpr int GAM = WGT + 4 * C * 4;          // float [4] factor of the state over the chunk
-  static constexpr int ANC = GAM + 16;                 // float [4][4] <S, dS> by compute wave
-  static constexpr int RX = ANC + 64;                  // float [4][4][C] state part . x by compute wave
-  static constexpr int RR = RX + (DG ? 16 * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
-  static constexpr int RC = RR + (DG ? 8 * C * 4 : 0);   // float [4][C] pair sums of the queries
+  static constexpr int ANC = GAM + 16;                 // float [4][NW] <S, dS> by compute wave
+  static constexpr int RX = ANC + 16 * NW;             // float [4][NW][C] state part . x by compute wave
+  static constexpr int RR = RX + (DG ? 4 * NW * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
+  static constexpr int RC = RR + (DG ? 8 * C * 4 : 0);       // float [4][C] pair sums of the queries
   static constexpr int BYTES = RC + (DG ? 4 * C * 4 : 0);
 };
 
 // ---------------------------------------------------------------------------
-// The walk.  Eight waves per (sequence or segment, head, block of 64 CT value
+// The walk.  NW + 4 waves per (sequence or segment, head, block of 16 NW value
 // columns), in four roles, meeting at one barrier per chunk:
-//   waves 0-3  compute: wave w owns 16 CT value columns and keeps its
-//              [128 x 16 CT] slice of the state in matrix-core accumulators
-//              (fp32) over the whole walk; accumulators of two stacked tiles
-//              are an operand of the next product as they are.  For chunk c:
-//              the outputs, transposed (rows = value columns), so that a lane
-//              stores four consecutive columns: S^T q, scaled by e^{G_i}, plus
-//              the pair matrix times v; then S <- e^{G_C} S + k^T (e^{G_C - G_j} v_j).
-//   waves 4-5  pair matrix of chunk c + 1, one 16-query tile each: the
-//              products with the keys up to it, scaled by e^{G_i - G_j}
-//   wave 6     the decays: prefix sums and factors of chunk c + 2; with DG the
-//              decays' gradient of chunk c - 1
-//   wave 7     copies tiles from global memory straight into LDS, NBUF - 1
-//              chunks ahead of the compute waves, which therefore never wait
-//              behind a copy of their own
-// One compute and one other wave share each SIMD.  Chunks are 32 tokens (16 in
-// fp32): with 64 the tiles of only two chunks fit beside the ones in use, and
-// the copies' latency showed.
+//   NW compute waves: wave w owns 16 value columns and keeps its [128 x 16]
+//              slice of the state in matrix-core accumulators (fp32) over the
+//              whole walk; accumulators of two stacked tiles are an operand of
+//              the next product as they are.  For chunk c: the outputs,
+//              transposed (rows = value columns), so that a lane stores four
+//              consecutive columns: S^T q, scaled by e^{G_i}, plus the pair
+//              matrix times v; then S <- e^{G_C} S + k^T (e^{G_C - G_j} v_j).
+//   two pair waves: the pair matrix of chunk c + 1 in 16-query tiles, the
+//              products with the keys up to them scaled by e^{G_i - G_j}
+//   a decay wave: prefix sums and factors of chunk c + 2; with DG the decays'
+//              gradient of chunk c - 1
+//   a loader:  copies tiles from global memory straight into LDS, up to
+//              NBUF - 1 chunks ahead of the compute waves, which therefore
+//              never wait behind a copy of their own
+// A wave issues at most one matrix product per 16 cycles and one vector
+// instruction per 4, half of what its SIMD can do (measured), and a compute
+// wave is bound by that; so a whole head takes eight waves of 16 columns
+// rather than four of 32 (where they measured 1.9 times as long per chunk),
+// and half a head, whose four waves have a SIMD each, takes longer chunks,
+// which need fewer instructions per token.
 // REV walks backwards in time: the pair matrix is upper triangular and the
 // factors of rows and of tokens change places.
 // DG (the decays' gradient): x is q in the dq walk and k in the dk walk.
 // ---------------------------------------------------------------------------
-template <typename E, int CT, bool REV, bool TR, bool OUT, bool DG>
-__global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p) {
-  using L = WalkLayout<E, CT, DG>;
+template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
+__global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
+  using L = WalkLayout<E, NW, DG>;
   using TF = typename Tok<E>::F;
   constexpr int TN = Tok<E>::N;
   constexpr int C = L::C, NT = C / 16, ES = L::ES, NBUF = L::NBUF;
@@ -346,7 +360,8 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   constexpr int NSS = (BF && DG) ? 3 : 1;      // terms of the state in the outputs' product
   constexpr bool DK = DG && REV;               // dk walk: forms the decays' gradient
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
-  static_assert(C == 4 * TN, "one token step per chunk");
+  constexpr int KT = C / (4 * TN);             // token steps per chunk
+  constexpr int TPS = NT / KT;                 // 16-token tiles per token step
   extern __shared__ __align__(16) unsigned char smem[];
   float* sSum = reinterpret_cast<float*>(smem + L::SUM);
   float* sRow = reinterpret_cast<float*>(smem + L::ROW);
@@ -359,7 +374,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int CB = 2 / CT;  // column blocks of a head
+  constexpr int CB = 8 / NW;  // column blocks of a head
   // blocks b and b + 8 run on the same XCD: a head's column blocks share its L2
   const int64_t slot8 = blockIdx.x >> 3;
   const int cb = (int)(slot8 % CB);
@@ -404,7 +419,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   // Iteration ci (from -1): compute waves on chunk ci, pair waves on ci + 1,
   // decay wave on ci + 2 and back on ci - 1, loader on ci + NBUF - 1.
 
-  if (wv == 7) {
+  if (wv == NW + 3) {
     // ---- loader ----
     // 1 KiB pieces, 16 bytes a lane; the lanes' offsets are the same in every
     // chunk.  Rows behind the end lie outside the buffer view and arrive as
@@ -450,7 +465,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     return;
   }
 
-  if (wv == 6) {
+  if (wv == NW + 2) {
     // ---- decays ----
     // rows behind the end lie outside the buffer view and read zero
     auto load_rows = [&](const float* src, int ci) -> float {
@@ -491,19 +506,23 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
       float part = 0.f;
       if (lane < C)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) part += sRX[(b * 4 + w) * C + lane];
+        for (int w = 0; w < NW; ++w) part += sRX[(b * NW + w) * C + lane];
       if constexpr (!REV) {
         if (in) p.row_dot[(size_t)(t0 + lane) * H + h] = part;
       } else {
         float keys = 0.f, queries = 0.f;
         if (lane < C) {
 #pragma unroll
-          for (int w = 0; w < NT; ++w) keys += sRR[(b * 2 + w) * C + lane];
+          for (int w = 0; w < (NT > 1 ? 2 : 1); ++w) keys += sRR[(b * 2 + w) * C + lane];
           queries = sRC[b * C + lane];
         }
         const int64_t tend = min(te, t0 + C);
         if (tend == te || (tend - bos) % p.seg == 0)
-          flow = (double)sAnc[b * 4] + (double)sAnc[b * 4 + 1] + (double)sAnc[b * 4 + 2] + (double)sAnc[b * 4 + 3];
+        {
+          flow = 0.0;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) flow += (double)sAnc[b * NW + w];
+        }
         const double s = suffix_sum<C>(in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0, lane);
         const double d = flow + s;
         if (in) {
@@ -540,79 +559,93 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     return;
   }
 
-  if (wv >= 4) {
+  if (wv >= NW) {
     // ---- pair matrix of chunk ci + 1, keys in rows: lane = query, four consecutive keys ----
-    const int rt = wv - 4;
-    const int q = 16 * rt + l16;
-    const uint32_t q_at = tile_at<E, D>(q, 8 * g), k_at = tile_at<E, D>(l16, 8 * g);
+    // wave p takes the query tiles p and NT - 1 - p, one from each end of the triangle
+    const int pw = wv - NW;
+    const uint32_t k_at = tile_at<E, D>(l16, 8 * g);
     for (int ci = -1; ci < nch; ++ci) {
       chunk_barrier();
-      if (!OUT || rt >= NT || ci + 1 >= nch) continue;
+      if (!OUT || pw >= NT || ci + 1 >= nch) continue;
       const uint32_t base = (uint32_t)((ci + 1) % NBUF) * L::SET;
-      unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * C * ES);
+      unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * L::RB);
       const int b = (ci + 1) & 3;
       const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
       const int nv = (int)min((int64_t)C, te - t0);
-      Frag<E> fq[4];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], smem, base + q_at, 32 * ks);
-      Frag<E> fx[DK ? 4 : 1];
-      if constexpr (DK)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], smem, base + L::X + q_at, 32 * ks);
       const float* gs = sSum + b * 2 * C;
-      const float gq = gs[q], gq_lo = gs[C + q];
-      float csum = 0.f;
+      f32x4 rsum[DK ? NT : 1];
 #pragma unroll
-      for (int kt = 0; kt < NT; ++kt) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, rsum = {0.f, 0.f, 0.f, 0.f};
-        // a tile beyond the triangle is zero
-        if (REV ? kt >= rt : kt <= rt) {
-          f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
+      for (int kt = 0; kt < (DK ? NT : 1); ++kt) rsum[kt] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            Frag<E> fk;
-            ld_row(fk, smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
-            acc = mma(acc, fk, fq[ks]);
-          }
-          if constexpr (DK)
+      for (int half = 0; half < (NT == 4 ? 2 : 1); ++half) {
+        const int rt = half ? NT - 1 - pw : pw;
+        const int q = 16 * rt + l16;
+        Frag<E> fq[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], smem, base + k_at + 16 * rt * (D * ES), 32 * ks);
+        Frag<E> fx[DK ? 4 : 1];
+        if constexpr (DK)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], smem, base + L::X + k_at + 16 * rt * (D * ES), 32 * ks);
+        const float gq = gs[q], gq_lo = gs[C + q];
+        float csum = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < NT; ++kt) {
+          const bool tri = REV ? kt >= rt : kt <= rt;
+          // a tile beyond the triangle that shares a token step with it is zero
+          if (!tri && kt / TPS != rt / TPS) continue;
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          if (tri) {
+            f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              Frag<E> fv;
-              ld_row(fv, smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
-              acc2 = mma(acc2, fv, fx[ks]);
+              Frag<E> fk;
+              ld_row(fk, smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
+              acc = mma(acc, fk, fq[ks]);
             }
-          const f32x4 gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
-          const f32x4 gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
+            if constexpr (DK)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = 16 * kt + 4 * g + i;
-            const bool on = REV ? (k >= q && k < nv) : k <= q;
-            const float d = (gq - gk[i]) + (gq_lo - gk_lo[i]);
-            const float e = acc[i] * exp2_fast(REV ? -d : d);
-            const float x = on ? e : 0.f;
-            if constexpr (DK) {
-              const float f = (on && k != q) ? x * acc2[i] : 0.f;
-              rsum[i] = f;
-              csum += f;
+              for (int ks = 0; ks < 4; ++ks) {
+                Frag<E> fv;
+                ld_row(fv, smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
+                acc2 = mma(acc2, fv, fx[ks]);
+              }
+            const f32x4 gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
+            const f32x4 gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 16 * kt + 4 * g + i;
+              const bool on = REV ? (k >= q && k < nv) : k <= q;
+              const float d = (gq - gk[i]) + (gq_lo - gk_lo[i]);
+              const float e = acc[i] * exp2_fast(REV ? -d : d);
+              const float x = on ? e : 0.f;
+              if constexpr (DK) {
+                const float f = (on && k != q) ? x * acc2[i] : 0.f;
+                rsum[kt][i] += f;
+                csum += f;
+              }
+              acc[i] = x;
             }
-            acc[i] = x;
           }
+          const uint32_t at = BF ? pair_at<L::RB>(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at<L::RB>(q, 4 * kt + g);
+          store_row4(reinterpret_cast<E*>(pair + at), acc);
         }
-        store_row4(reinterpret_cast<E*>(pair + (BF ? pair_at(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at(q, g))), acc);
         if constexpr (DK) {
-          // over the 16 queries of the tile
-#pragma unroll
-          for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rsum[i] += __shfl_xor(rsum[i], m);
-          if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + rt) * C + 16 * kt + 4 * g) = rsum;
+          csum += __shfl_xor(csum, 16);
+          csum += __shfl_xor(csum, 32);
+          if (g == 0) sRC[b * C + q] = csum;
         }
       }
       if constexpr (DK) {
-        csum += __shfl_xor(csum, 16);
-        csum += __shfl_xor(csum, 32);
-        if (g == 0) sRC[b * C + q] = csum;
+        // over the 16 queries of a tile
+#pragma unroll
+        for (int kt = 0; kt < NT; ++kt) {
+#pragma unroll
+          for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rsum[kt][i] += __shfl_xor(rsum[kt][i], m);
+          if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + pw) * C + 16 * kt + 4 * g) = rsum[kt];
+        }
       }
     }
     if constexpr (DG) chunk_barrier();
@@ -620,40 +653,36 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   }
 
   // ---- compute ----
-  const int vc0 = 16 * CT * wv;          // first value column within the block
+  const int vc0 = 16 * wv;               // first value column within the block
   const int col0 = cb * L::VW + vc0;     // and within the head
-  // state element (row, column) of this walk in a stored state
-  auto state_at = [&](int row, int col) { return TR ? col * D + row : row * D + col; };
-  auto load_state = [&](const float* src, f32x4 (&s)[CT][8]) {
+  // The state slice: tile rt holds rows 16 rt + 4 g + i of column col0 + l16;
+  // TR: of the transpose of what is stored.
+  auto load_state = [&](const float* src, f32x4 (&s)[8]) {
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int rt = 0; rt < 8; ++rt) {
+      const int row = 16 * rt + 4 * g, col = col0 + l16;
+      if constexpr (TR) {
+        s[rt] = *reinterpret_cast<const f32x4*>(src + col * D + row);
+      } else {
 #pragma unroll
-      for (int rt = 0; rt < 8; ++rt) {
-        const int row = 16 * rt + 4 * g, col = col0 + 16 * c + l16;
-        if constexpr (TR) {
-          s[c][rt] = *reinterpret_cast<const f32x4*>(src + state_at(row, col));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[c][rt][i] = src[state_at(row + i, col)];
-        }
+        for (int i = 0; i < 4; ++i) s[rt][i] = src[(row + i) * D + col];
       }
+    }
   };
-  auto store_state = [&](float* dst, const f32x4 (&s)[CT][8]) {
+  auto store_state = [&](float* dst, const f32x4 (&s)[8]) {
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int rt = 0; rt < 8; ++rt) {
+      const int row = 16 * rt + 4 * g, col = col0 + l16;
+      if constexpr (TR) {
+        *reinterpret_cast<f32x4*>(dst + col * D + row) = s[rt];
+      } else {
 #pragma unroll
-      for (int rt = 0; rt < 8; ++rt) {
-        const int row = 16 * rt + 4 * g, col = col0 + 16 * c + l16;
-        if constexpr (TR) {
-          *reinterpret_cast<f32x4*>(dst + state_at(row, col)) = s[c][rt];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[state_at(row + i, col)] = s[c][rt][i];
-        }
+        for (int i = 0; i < 4; ++i) dst[(row + i) * D + col] = s[rt][i];
       }
+    }
   };
   constexpr size_t kState = (size_t)D * D;
-  f32x4 accS[CT][8];
+  f32x4 accS[8];
   {
     const float* src = nullptr;
     if (OUT) {
@@ -666,9 +695,7 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
       load_state(src, accS);
     } else {
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int rt = 0; rt < 8; ++rt) accS[c][rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < 8; ++rt) accS[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
   }
   // lane offsets within the tiles and the output rows
@@ -676,7 +703,9 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   col_at<D>(k_at, static_cast<const E*>(nullptr), 0, l16, g);
   col_at<L::VW>(v_at, static_cast<const E*>(nullptr), vc0, l16, g);
   const uint32_t q_at = tile_at<E, D>(l16, 4 * g), x_at = tile_at<E, D>(l16, col0 + 4 * g);
-  const uint32_t p_at = pair_at(l16, g);
+  uint32_t p_at[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) p_at[kt] = pair_at<L::RB>(l16, 4 * kt + g);
   const int oes = TR && p.o_f32 ? 4 : ES;
   const uint32_t o_row = (uint32_t)H * (D * oes);
   const uint32_t o_at = (uint32_t)l16 * o_row + (uint32_t)((col0 + 4 * g) * oes);
@@ -705,19 +734,16 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
       const int64_t tend = t0 + nv;
       if (tend == te || (tend - bos) % p.seg == 0) {
         const int64_t sl = slot_of(n, bos, p.seg, (tend - bos + p.seg - 1) / p.seg);
-        const float* src = p.fwd_snap + ((size_t)sl * H + h) * kState;
+        f32x4 x[8];
+        load_state(p.fwd_snap + ((size_t)sl * H + h) * kState, x);
         float dot = 0.f;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int rt = 0; rt < 8; ++rt)
 #pragma unroll
-          for (int rt = 0; rt < 8; ++rt) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(src + state_at(16 * rt + 4 * g, col0 + 16 * c + l16));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dot += x[i] * accS[c][rt][i];
-          }
+          for (int i = 0; i < 4; ++i) dot += x[rt][i] * accS[rt][i];
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m);
-        if (lane == 0) sAnc[b * 4 + wv] = dot;
+        if (lane == 0) sAnc[b * NW + wv] = dot;
       }
     }
     chunk_barrier();
@@ -727,135 +753,128 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
     // fills the gaps between products.
     const uint32_t base_next = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
     const float gam = sGam[b];
-    float w[TN];
+    float w[KT][TN];
+    TF fv[KT], fk[8];
 #pragma unroll
-    for (int i = 0; i < TN; i += 4) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + TN * g + i);
+    for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[i + j] = y[j];
+      for (int i = 0; i < TN; i += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + 4 * TN * kt + TN * g + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
+      }
+      ld_col(fv[kt], smem, base + L::V + kt * (4 * TN * L::VW * ES), v_at, 0);
     }
-    TF fv[CT], fk[8];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) ld_col(fv[c], smem, base + L::V, v_at, 16 * c);
-    auto read_k = [&](int first, int count) {
+    auto read_k = [&](int kt, int first, int count) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt)
-        if (rt >= first && rt < first + count) ld_col(fk[rt], smem, base + L::K, k_at, 16 * rt);
-    };
-    auto decay_state = [&](int rt) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c) accS[c][rt] *= gam;
+        if (rt >= first && rt < first + count) ld_col(fk[rt], smem, base + L::K + kt * (4 * TN * D * ES), k_at, 16 * rt);
     };
     // values times their factors, in the terms of the state's update
-    TF fw[CT][NSV];
-    auto weigh_values = [&]() {
+    TF fw[KT][NSV];
+    auto weigh_values = [&](int kt) {
+      float x[TN];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        float x[TN];
-#pragma unroll
-        for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[c], i) * w[i];
-        split<NSV>(fw[c], x);
-      }
+      for (int i = 0; i < TN; ++i) x[i] = frag_get(fv[kt], i) * w[kt][i];
+      split<NSV>(fw[kt], x);
     };
-    f32x4 accO[OUT ? CT : 1][NT];
+    auto add_to_state = [&](int kt) {
+#pragma unroll
+      for (int s = 0; s < NSV; ++s)
+#pragma unroll
+        for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][s]);
+    };
+    f32x4 accO[OUT ? NT : 1];
     if constexpr (OUT) {
       // outputs (transposed: lane = token, four consecutive value columns)
-      TF fp[NT];
       float row[NT];
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) row[rt] = sRow[b * C + 16 * rt + l16];
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt)
-        ld_pair(fp[rt], smem, L::PAIR + (ci & 1) * (C * C * ES) + p_at + 16 * rt * 64);
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int rt = 0; rt < NT; ++rt) accO[c][rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int rt = 0; rt < NT; ++rt) accO[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        Frag<E> fs[CT][NSS];
+        Frag<E> fs[NSS];
+        float x[8];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = accS[c][2 * ks][i];
-            x[4 + i] = accS[c][2 * ks + 1][i];
-          }
-          split<NSS>(fs[c], x);
+        for (int i = 0; i < 4; ++i) {
+          x[i] = accS[2 * ks][i];
+          x[4 + i] = accS[2 * ks + 1][i];
         }
+        split<NSS>(fs, x);
 #pragma unroll
         for (int s = 0; s < NSS; ++s)
 #pragma unroll
-          for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-            for (int c = 0; c < CT; ++c) accO[c][rt] = mma(accO[c][rt], fs[c][s], fq[ks][rt]);
-        decay_state(2 * ks);
-        decay_state(2 * ks + 1);
-        if (ks >= 2) read_k(2 * (ks - 2), 2);
+          for (int rt = 0; rt < NT; ++rt) accO[rt] = mma(accO[rt], fs[s], fq[ks][rt]);
+        accS[2 * ks] *= gam;
+        accS[2 * ks + 1] *= gam;
+        if (ks >= 2) read_k(0, 2 * (ks - 2), 2);
         __builtin_amdgcn_sched_barrier(0);
       }
-      weigh_values();
-      read_k(4, 4);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        float dot = 0.f;
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          accO[c][rt] *= row[rt];
-          if constexpr (DG) {
-            Frag16<E> fx;
-            ld_frag16(fx, reinterpret_cast<const E*>(smem + ((base + L::X + x_at) ^ (uint32_t)(16 * c * ES)) + 16 * rt * (D * ES)));
-            const f32x4 x = frag16_to_f32(fx);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dot += x[i] * accO[c][rt][i];
-          }
-        }
-        if constexpr (DG) {
-          dot += __shfl_xor(dot, 16);
-          dot += __shfl_xor(dot, 32);
-          if (g == 0) sRX[(b * 4 + wv) * C + 16 * rt + l16] = dot;
-        }
-      }
+      for (int kt = 0; kt < KT; ++kt) weigh_values(kt);
+      TF fp[NT][KT];
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) accO[c][rt] = mma_tok(accO[c][rt], fv[c], fp[rt]);
-    } else {
-      read_k(0, 8);
+        for (int kt = 0; kt < KT; ++kt)
+          if (REV ? kt >= rt / TPS : kt <= rt / TPS)
+            ld_pair(fp[rt][kt], smem, L::PAIR + (ci & 1) * (C * L::RB) + p_at[kt] + 16 * rt * L::RB);
+      read_k(0, 4, 4);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int rt = 0; rt < 8; ++rt) decay_state(rt);
-      weigh_values();
+      for (int rt = 0; rt < NT; ++rt) {
+        accO[rt] *= row[rt];
+        if constexpr (DG) {
+          float dot = 0.f;
+          Frag16<E> fx;
+          ld_frag16(fx, reinterpret_cast<const E*>(smem + base + L::X + x_at + 16 * rt * (D * ES)));
+          const f32x4 x = frag16_to_f32(fx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot += x[i] * accO[rt][i];
+          dot += __shfl_xor(dot, 16);
+          dot += __shfl_xor(dot, 32);
+          if (g == 0) sRX[(b * NW + wv) * C + 16 * rt + l16] = dot;
+        }
+      }
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt)
+          if (REV ? kt >= rt / TPS : kt <= rt / TPS) accO[rt] = mma_tok(accO[rt], fv[kt], fp[rt][kt]);
+    } else {
+      read_k(0, 0, 8);
+#pragma unroll
+      for (int rt = 0; rt < 8; ++rt) accS[rt] *= gam;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) weigh_values(kt);
     }
     // state, with the outputs' stores in between
-#pragma unroll
-    for (int s = 0; s < NSV; ++s)
-#pragma unroll
-      for (int rt = 0; rt < 8; ++rt)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) accS[c][rt] = mma_tok(accS[c][rt], fk[rt], fw[c][s]);
+    add_to_state(0);
+    if constexpr (KT == 2) {
+      read_k(1, 0, 8);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if constexpr (OUT) {
-      // the next chunk's queries: its tiles are in LDS already (the last chunk
-      // reads what is there and drops it)
-      read_q(base_next);
       // rows behind the end fall outside the buffer view and are dropped
       const Rsrc orb = make_rsrc(static_cast<char*>(p.o) + ((size_t)t0 * H + h) * (D * oes),
                                  (uint32_t)(nv - 1) * o_row + D * oes);
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int off = (int)(o_at + 16 * rt * o_row + 16 * c * oes);
-          if (!BF || (TR && p.o_f32)) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, accO[c][rt]), orb, off, 0, 0);
-          } else {
-            const f32x4 t = accO[c][rt];
-            const bf16x4 y = (bf16x4){(__bf16)t[0], (__bf16)t[1], (__bf16)t[2], (__bf16)t[3]};
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), orb, off, 0, 0);
-          }
+      for (int rt = 0; rt < NT; ++rt) {
+        const int off = (int)(o_at + 16 * rt * o_row);
+        if (!BF || (TR && p.o_f32)) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, accO[rt]), orb, off, 0, 0);
+        } else {
+          const f32x4 t = accO[rt];
+          const bf16x4 y = (bf16x4){(__bf16)t[0], (__bf16)t[1], (__bf16)t[2], (__bf16)t[3]};
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), orb, off, 0, 0);
         }
+      }
     }
+    if constexpr (KT == 2) add_to_state(1);
+    // the next chunk's queries: its tiles are in LDS already (the last chunk
+    // reads what is there and drops it)
+    read_q(base_next);
     base = base_next;
   }
   if constexpr (DG) chunk_barrier();  // the last chunk's sums
@@ -869,40 +888,40 @@ __global__ __launch_bounds__(512) void linear_walk_kernel(const LinearWalkArgs p
   }
 }
 
-template <typename E, int CT, bool REV, bool TR, bool OUT, bool DG>
+template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
 hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
-  using L = WalkLayout<E, CT, DG>;
-  constexpr int CB = 2 / CT;
+  using L = WalkLayout<E, NW, DG>;
+  constexpr int CB = 8 / NW;
   const int64_t blocks = (a.units + 7) / 8 * 8 * CB;
   static std::atomic<bool> set[64];
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(linear_walk_kernel<E, CT, REV, TR, OUT, DG>),
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(linear_walk_kernel<E, NW, REV, TR, OUT, DG>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL((linear_walk_kernel<E, CT, REV, TR, OUT, DG>), dim3((unsigned)blocks), dim3(512), L::BYTES, stream, a);
+  hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, TR, OUT, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), L::BYTES, stream, a);
   return hipGetLastError();
 }
 
 template <typename E>
 hipError_t launch_walk_e(const LinearWalkArgs& a, hipStream_t stream) {
   if (!a.write_o)
-    return a.reverse ? launch_walk_t<E, 2, true, false, false, false>(a, stream)
-                     : launch_walk_t<E, 2, false, false, false, false>(a, stream);
+    return a.reverse ? launch_walk_t<E, 8, true, false, false, false>(a, stream)
+                     : launch_walk_t<E, 8, false, false, false, false>(a, stream);
   if (a.transposed) {
     if (a.reverse)
-      return a.with_decay_grad ? launch_walk_t<E, 2, true, true, true, true>(a, stream)
-                               : launch_walk_t<E, 2, true, true, true, false>(a, stream);
-    return a.with_decay_grad ? launch_walk_t<E, 2, false, true, true, true>(a, stream)
-                             : launch_walk_t<E, 2, false, true, true, false>(a, stream);
+      return a.with_decay_grad ? launch_walk_t<E, 8, true, true, true, true>(a, stream)
+                               : launch_walk_t<E, 8, true, true, true, false>(a, stream);
+    return a.with_decay_grad ? launch_walk_t<E, 8, false, true, true, true>(a, stream)
+                             : launch_walk_t<E, 8, false, true, true, false>(a, stream);
   }
-  if (a.reverse) return launch_walk_t<E, 2, true, false, true, false>(a, stream);
-  return a.narrow ? launch_walk_t<E, 1, false, false, true, false>(a, stream)
-                  : launch_walk_t<E, 2, false, false, true, false>(a, stream);
+  if (a.reverse) return launch_walk_t<E, 8, true, false, true, false>(a, stream);
+  return a.narrow ? launch_walk_t<E, 4, false, false, true, false>(a, stream)
+                  : launch_walk_t<E, 8, false, false, true, false>(a, stream);
 }
 
 // ---------------------------------------------------------------------------

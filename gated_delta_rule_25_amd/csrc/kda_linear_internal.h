@@ -7,9 +7,6 @@
 
 namespace kda {
 
-// Tokens per chunk: one chunk's query or key tile is 8 KiB.
-constexpr int linear_chunk_len(bool bf16) { return bf16 ? 32 : 16; }
-
 // Segments.  Every sequence is cut into segments of `seg` tokens (a multiple
 // of 64) counted from its own start; segment j of sequence n has the slot
 //   cu[n] / seg + 2 n + j.
