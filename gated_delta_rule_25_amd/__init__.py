@@ -98,6 +98,12 @@ def _load():
     lib.kda_linear_chunk_bwd.argtypes = [vp] * 8 + [i32, i64] + [i32] * 7 + [vp] * 6 + [sz, vp]
     lib.kda_linear_decode_step.restype = i32
     lib.kda_linear_decode_step.argtypes = [vp] * 5 + [i32] * 7 + [vp, vp]
+    lib.kda_beam_select_workspace_bytes.restype = sz
+    lib.kda_beam_select_workspace_bytes.argtypes = [i32] * 4
+    lib.kda_beam_select.restype = i32
+    lib.kda_beam_select.argtypes = [vp] * 3 + [i32] * 5 + [vp] * 5 + [sz, vp]
+    lib.kda_beam_reorder.restype = i32
+    lib.kda_beam_reorder.argtypes = [vp, vp, i32, vp, i32, i32, vp]
     lib.kda_decode_replay.restype = i32
     lib.kda_decode_replay.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp,
                                       vp, vp]
@@ -543,3 +549,7 @@ from .linear import (chunk_linear, linear_chunk_bwd, linear_chunk_bwd_workspace_
 
 __all__ += ["linear_chunk_fwd", "linear_chunk_bwd", "chunk_linear", "linear_decode_step",
             "linear_chunk_fwd_workspace_bytes", "linear_chunk_bwd_workspace_bytes"]
+
+from .beam import BEAM_MAX, beam_reorder, beam_select, beam_select_workspace_bytes  # noqa: E402
+
+__all__ += ["beam_select", "beam_reorder", "beam_select_workspace_bytes", "BEAM_MAX"]

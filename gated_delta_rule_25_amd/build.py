@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libkda.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_replay.hip", "kda_debug.hip", "kda_scan.hip", "kda_chunk.hip", "kda_prep.hip",
-           "kda_bwd.hip", "kda_linear.hip", "kda_linear_decode.hip", "kda_linear_api.hip"]
+           "kda_bwd.hip", "kda_linear.hip", "kda_linear_decode.hip", "kda_linear_api.hip", "kda_beam.hip",
+           "kda_beam_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

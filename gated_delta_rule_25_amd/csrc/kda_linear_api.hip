@@ -21,7 +21,7 @@ constexpr int kMaxHeads = 65535;
 // Longest stretch over which the decays' gradient is summed token by token
 // before it is taken from the states again.
 constexpr int64_t kAnchorTokens = 1024;
-constexpr int64_t kMinSegment = 256;
+constexpr int64_t kMinSegment = 512;
 
 bool linear_sizes_ok(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads) {
   return num_seqs >= 1 && num_heads >= 1 && num_heads <= kMaxHeads && num_qk_heads >= 1 &&
@@ -38,6 +38,17 @@ struct LinearPlan {
   size_t bytes = 0;
 };
 
+// Whether sequences are cut into segments that run side by side, and how
+// long those are.  One workgroup fills a compute unit, so a walk per
+// (sequence, head) leaves units idle when there are fewer chains than units;
+// segments cost a pass for their contributions (two in the backward pass) and
+// their states' traffic.  Forward: from three units per chain on, one segment
+// per unit (8 heads x 131072 tokens: 380 us in segments of 4096 against 448 at
+// 1024 and 3726 us in one walk; 96 heads x 8192: 280 us in one walk of half
+// heads against 330 at 1024).  Backward, three walks: whenever chains are
+// fewer than units, three segments per unit, of 512 tokens at least (96 heads
+// x 8192: 1036 us in segments of 1024 against 1573 in one walk; 9 ragged
+// sequences of 4927 tokens x 16 heads: 202 us at 512, 229 at 256, 560 in one).
 void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
                      bool backward) {
   const int64_t units = (int64_t)num_seqs * num_heads;
@@ -45,9 +56,9 @@ void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num
   if (segment_tokens > 0) {
     pl.segmented = true;
     pl.seg = segment_tokens;
-  } else if (segment_tokens == 0 && 3 * units < cus) {
-    const int64_t target = (2 * cus + num_heads - 1) / num_heads;
-    int64_t seg = (total_tokens + target - 1) / target;
+  } else if (segment_tokens == 0 && (backward ? units : 3 * units) < cus) {
+    const int64_t target = (int64_t)cus * (backward ? 3 : 1);
+    int64_t seg = (total_tokens * num_heads + target - 1) / target;
     seg = std::max((seg + 63) / 64 * 64, kMinSegment);
     if ((int64_t)num_seqs * seg < total_tokens) {
       pl.segmented = true;
