@@ -17,10 +17,10 @@
 //                      the sum of exponentials (exponentials of differences
 //                      to the thread's own maximum, fp32; combined in fp64).
 //                      Bound by HBM.
-//   beam_pick_kernel   one workgroup per group, a wave per beam: the K best
-//                      parts, their elements read again (K x nv vectors), the
-//                      row's K best; then one wave takes the K best of the
-//                      K x K candidates, compared as fp64 scores.
+//   beam_pick_kernel   one workgroup per group: the K best parts of each row,
+//                      their elements read again (K x nv vectors), the row's
+//                      K best; then one wave takes the K best of the K x K
+//                      candidates, compared as fp64 scores.
 // Nothing depends on the order in which workgroups run.
 //
 // Reordering.  Row n of a group's states becomes the row of its parent.  A
@@ -49,17 +49,38 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t key_at(uint64_t key) { return ~(uint32_t)key; }
 
+// Largest of a wave's numbers, in every lane (lane moves within rows of 16,
+// then between them: no LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xf, false);
+  const uint64_t o = (uint64_t)hi << 32 | lo;
+  return o > x ? o : x;
+}
 __device__ __forceinline__ uint64_t wave_max(uint64_t x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)x, m);
-    x = o > x ? o : x;
-  }
-  return x;
+  x = dpp_max<0x111, 0xf>(x);  // from the lane 1, 2, 4, 8 below
+  x = dpp_max<0x112, 0xf>(x);
+  x = dpp_max<0x114, 0xf>(x);
+  x = dpp_max<0x118, 0xf>(x);
+  x = dpp_max<0x142, 0xa>(x);  // from the last lane of the row below
+  x = dpp_max<0x143, 0xc>(x);  // from the last lane of the lower half
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), 63);
+  return (uint64_t)hi << 32 | lo;
+}
+// an fp64 number as an integer of the same order
+__device__ __forceinline__ uint64_t double_key(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_double(uint64_t k) {
+  return __builtin_bit_cast(double, (k >> 63) ? k ^ 0x8000000000000000ull : ~k);
 }
 
-// NaN is a masked logit like -inf; +inf counts as the largest number.
-__device__ __forceinline__ float beam_logit(float x) { return fminf(x == x ? x : -INFINITY, FLT_MAX); }
+// NaN is a masked logit like -inf (the maximum of NaN and a number is the
+// number); +inf counts as the largest finite number.
+__device__ __forceinline__ float beam_logit(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
 template <typename E>
 __device__ __forceinline__ float load_logit(const E* p) { return beam_logit(to_f32(*p)); }
 
@@ -106,6 +127,10 @@ __device__ __forceinline__ bool row_is_read(const BeamSelectArgs& a, int64_t row
   return a.scores[row] > -INFINITY && !(a.finished && a.finished[row]);
 }
 
+// e^x for x <= 0.  The product's rounding moves a term by |x| 2^-24 of it, and
+// terms of large |x| are small: the sum's error stays near its own rounding.
+__device__ __forceinline__ float beam_exp(float x) { return exp2_fast(x * 1.44269504f); }
+
 // One workgroup per (row, slice).
 template <typename E>
 __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelectArgs a) {
@@ -129,7 +154,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelec
   float top = -INFINITY;
   auto fold = [&](float m) {
     if (m > top) {
-      sum *= top > -INFINITY ? __expf(top - m) : 0.f;
+      sum *= top > -INFINITY ? beam_exp(top - m) : 0.f;
       top = m;
     }
   };
@@ -153,7 +178,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelec
     if (m > -INFINITY) {
       fold(m);
 #pragma unroll
-      for (int j = 0; j < U; ++j) sum += expf(v[j] - top);
+      for (int j = 0; j < U; ++j) sum += beam_exp(v[j] - top);
     } else if (at == INT32_MAX) {
       at = e0;
     }
@@ -165,7 +190,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelec
       take(v, i);
       if (v > -INFINITY) {
         fold(v);
-        sum += expf(v - top);
+        sum += beam_exp(v - top);
       }
     }
   }
@@ -181,7 +206,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelec
   if ((t & 63) == 0) sm[t >> 6] = m;
   __syncthreads();
   m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  double d = top > -INFINITY ? (double)sum * (double)expf(top - m) : 0.0;
+  double d = top > -INFINITY ? (double)sum * (double)beam_exp(top - m) : 0.0;
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) d += __shfl_xor(d, k);
   if ((t & 63) == 0) ss[t >> 6] = d;
@@ -192,15 +217,34 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(const BeamSelec
   }
 }
 
-struct BeamCandidate {
-  double score;
-  uint64_t at;  // beam * vocab + token
-};
-__device__ __forceinline__ bool better(const BeamCandidate& a, const BeamCandidate& b) {
-  return a.score > b.score || (a.score == b.score && a.at < b.at);
+// Largest of a wave's numbers (not NaN), in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_fmax(float x) {
+  const int o = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, -INFINITY), __builtin_bit_cast(int, x), CTRL, ROWS,
+                                            0xf, false);
+  return fmaxf(x, __builtin_bit_cast(float, o));
+}
+__device__ __forceinline__ float wave_fmax(float x) {
+  x = dpp_fmax<0x111, 0xf>(x);
+  x = dpp_fmax<0x112, 0xf>(x);
+  x = dpp_fmax<0x114, 0xf>(x);
+  x = dpp_fmax<0x118, 0xf>(x);
+  x = dpp_fmax<0x142, 0xa>(x);
+  x = dpp_fmax<0x143, 0xc>(x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 
 // One workgroup per group, wave k for beam k.
+//   1. The C = min(K, V) best parts.  A lane holds up to 32; the C-th largest
+//      of the lanes' own maxima is a bound that at least C parts reach, and
+//      seldom many more: those move to one a lane, where C rounds of the
+//      wave's maximum sort them out.  (Ties beyond 64 parts take the rounds
+//      over all parts.)
+//   2. Their largest elements are C elements of the row, so none below the
+//      last of them is wanted.
+//   3. The C parts are read again; where one holds another element that is
+//      wanted (seldom), the list of the C best is formed anew with it.
+// Then one wave takes the K best of the K x C candidates.
 template <typename E>
 __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSelectArgs a) {
   constexpr int U = 16 / (int)sizeof(E);
@@ -209,146 +253,207 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
   const int g = blockIdx.x, lane = threadIdx.x & 63;
   const int k = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = (int64_t)g * K + k;
-  __shared__ BeamCandidate cand[kBeamMax * kBeamMax];
+  __shared__ uint64_t few_key[kBeamMax][64];
+  __shared__ int few_id[kBeamMax][64];
+  __shared__ double cand_score[kBeamMax * kBeamMax];
+  __shared__ uint64_t cand_at[kBeamMax * kBeamMax];  // beam << 32 | token: the order of beam * vocab + token
   __shared__ uint8_t done[kBeamMax];
   const float score = a.scores[row];
   const bool fin = a.finished && a.finished[row];
-  if (lane == 0) done[k] = fin;
   const int C = min(K, V);  // candidates of a row
-  BeamCandidate mine = {-INFINITY, 0};  // lane i < C: the row's i-th best
-  if (!row_is_read(a, row)) {
-    // the end token if the beam is finished (a beam without a score ties at
-    // -inf with everything), then the lowest tokens at -inf
-    const bool ends = fin && score > -INFINITY && a.end_token >= 0 && a.end_token < V;
-    int t = lane;
-    if (ends) t = lane == 0 ? a.end_token : (lane - 1 < a.end_token ? lane - 1 : lane);
-    mine.score = ends && lane == 0 ? (double)score : -INFINITY;
-    mine.at = (uint64_t)k * V + t;
-  } else {
-    // log of the row's sum of exponentials
-    float m = -INFINITY;
-    for (int s = lane; s < a.plan.slices; s += 64) m = fmaxf(m, a.slice_max[row * a.plan.slices + s]);
+  const int parts = a.plan.slices * kBeamThreads;
+  {
+    double mine = -INFINITY;  // lane i < C: the row's i-th best
+    uint64_t at = 0;
+    if (!row_is_read(a, row)) {
+      // the end token if the beam is finished (a beam without a score ties at
+      // -inf with everything), then the lowest tokens at -inf
+      const bool ends = fin && score > -INFINITY && a.end_token >= 0 && a.end_token < V;
+      int t = lane;
+      if (ends) t = lane == 0 ? a.end_token : (lane - 1 < a.end_token ? lane - 1 : lane);
+      if (ends && lane == 0) mine = (double)score;
+      at = (uint64_t)k << 32 | (uint32_t)t;
+    } else {
+      // all loads before the first use: they are in flight together
+      const float* pm = a.part_max + row * parts;
+      const int32_t* pa = a.part_at + row * parts;
+      float top[PL];
+      int where[PL];
 #pragma unroll
-    for (int i = 32; i >= 1; i >>= 1) m = fmaxf(m, __shfl_xor(m, i));
-    double sum = 0.0;
-    if (m > -INFINITY)
-      for (int s = lane; s < a.plan.slices; s += 64) {
-        const float sm = a.slice_max[row * a.plan.slices + s];
-        if (sm > -INFINITY) sum += (double)a.slice_sum[row * a.plan.slices + s] * exp((double)sm - (double)m);
+      for (int i = 0; i < PL; ++i) {
+        const int p = min(64 * i + lane, parts - 1);
+        top[i] = pm[p];
+        where[i] = pa[p];
       }
+      const int sl = min(lane, a.plan.slices - 1);
+      const float sm = lane < a.plan.slices ? a.slice_max[row * a.plan.slices + sl] : -INFINITY;
+      const float ssum = lane < a.plan.slices ? a.slice_sum[row * a.plan.slices + sl] : 0.f;
+      // log of the row's sum of exponentials
+      const float m = wave_fmax(sm);
+      double sum = sm > -INFINITY ? (double)ssum * exp((double)sm - (double)m) : 0.0;
 #pragma unroll
-    for (int i = 32; i >= 1; i >>= 1) sum += __shfl_xor(sum, i);
-    const double lse = (double)m + log(sum);
-    // the C best parts
-    const int64_t parts = (int64_t)a.plan.slices * kBeamThreads;
-    uint64_t pk[PL];
+      for (int i = 32; i >= 1; i >>= 1) sum += __shfl_xor(sum, i);
+      const double lse = (double)m + log(sum);
+      // a bound that C parts reach
+      float most = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int64_t p = lane + 64 * i;
-      pk[i] = 0;
-      if (p < parts) {
-        const int at = a.part_at[row * parts + p];
-        if (at != INT32_MAX) pk[i] = beam_key(a.part_max[row * parts + p], (uint32_t)at);
+      for (int i = 0; i < PL; ++i) {
+        if (64 * i + lane >= parts) where[i] = INT32_MAX;
+        if (where[i] != INT32_MAX) most = fmaxf(most, top[i]);
       }
-    }
-    const E* x = static_cast<const E*>(a.logits) + row * V;
-    const BeamRow r = beam_row(x, V);
-    int part = -1;  // lane i < C: the i-th best part
-    uint64_t last = ~0ull;
-    for (int c = 0; c < C; ++c) {
-      uint64_t b = 0;
-      int bi = 0;
+      float bound = -INFINITY;
+      for (int c = 0; c < C;) {
+        bound = wave_fmax(most);
+        if (!(bound > -INFINITY)) break;
+        c += __popcll(__ballot(most == bound));
+        if (most == bound) most = -INFINITY;
+      }
+      int few = 0;
 #pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (pk[i] < last && pk[i] > b) {
-          b = pk[i];
-          bi = i;
+      for (int i = 0; i < PL; ++i) {
+        const bool in = where[i] != INT32_MAX && top[i] >= bound;
+        const uint64_t mask = __ballot(in);
+        if (mask != 0) {
+          const int to = few + __popcll(mask & ((1ull << lane) - 1));
+          if (in && to < 64) {
+            few_key[k][to] = beam_key(top[i], (uint32_t)where[i]);
+            few_id[k][to] = 64 * i + lane;
+          }
+          few += __popcll(mask);
         }
-      const uint64_t w = wave_max(b);
-      if (w == 0) break;  // fewer parts than candidates
-      const uint64_t who = __ballot(b == w);
-      const int src = __ffsll((unsigned long long)who) - 1;
-      const int got = __shfl(lane + 64 * bi, src);
-      if (lane == c) part = got;
-      last = w;
-    }
-    // their elements: vector j of part i is lane (64 a turn); the list of the
-    // best so far stays with the lanes 0 .. C - 1
-    uint64_t list = 0;
-    auto merge = [&](const uint64_t* key, int count) {
-      uint64_t keep = 0, before = ~0ull;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+      uint64_t list = 0;  // lane i < C: the i-th best element
+      int part = -1;      // and the part it is from
+      uint64_t least = 0;
+      uint64_t cur = 0;
+      int id = -1;
+      if (few <= 64 && lane < few) {
+        cur = few_key[k][lane];
+        id = few_id[k][lane];
+      }
+      uint64_t before = ~0ull;
       for (int c = 0; c < C; ++c) {
-        uint64_t b = list < before ? list : 0;
-        for (int i = 0; i < count; ++i)
-          if (key[i] < before && key[i] > b) b = key[i];
-        b = wave_max(b);
-        if (lane == c) keep = b;
-        before = b;
-        if (b == 0) break;
-      }
-      list = keep;
-    };
-    const int nv = a.plan.nv;
-    for (int v0 = 0; v0 < C * nv; v0 += 64) {
-      const int id = v0 + lane;
-      const int owner = __shfl(part, min(id / nv, C - 1));
-      uint64_t key[U + 1];
+        if (few > 64) {
+          cur = 0;
 #pragma unroll
-      for (int j = 0; j <= U; ++j) key[j] = 0;
-      if (id < C * nv && owner >= 0) {
-        const int slice = owner / kBeamThreads, t = owner % kBeamThreads;
-        const int vec = slice * kBeamThreads * nv + (id % nv) * kBeamThreads + t;
-        if (vec < r.nvec) {
-          const int e0 = r.head + vec * U;
-#pragma unroll
-          for (int j = 0; j < U; ++j) key[j] = beam_key(load_logit(x + e0 + j), (uint32_t)(e0 + j));
+          for (int i = 0; i < PL; ++i) {
+            const uint64_t key = where[i] != INT32_MAX ? beam_key(top[i], (uint32_t)where[i]) : 0;
+            if (key < before && key > cur) {
+              cur = key;
+              id = 64 * i + lane;
+            }
+          }
         }
-        if (id % nv == 0 && slice == 0) {
-          const int i = beam_extra<E>(r, V, t);
-          if (i >= 0) key[U] = beam_key(load_logit(x + i), (uint32_t)i);
+        const uint64_t w = wave_max(cur);
+        if (w == 0) break;  // fewer parts than candidates
+        const int src = __ffsll((unsigned long long)__ballot(cur == w)) - 1;
+        const int got = __builtin_amdgcn_readlane(id, src);
+        if (lane == c) {
+          list = w;
+          part = got;
         }
+        if (cur == w) cur = 0;
+        before = w;
+        if (c == C - 1) least = w;
       }
-      merge(key, U + 1);
+      // their elements: vector j of part i is lane i nv + j (64 a turn)
+      const E* x = static_cast<const E*>(a.logits) + row * V;
+      const BeamRow r = beam_row(x, V);
+      const int nv = a.plan.nv;
+      for (int v0 = 0; v0 < C * nv; v0 += 64) {
+        const int vid = v0 + lane;
+        const int i = min(vid / nv, C - 1);
+        const int owner = __shfl(part, i);
+        uint64_t key[U + 1];
+#pragma unroll
+        for (int j = 0; j <= U; ++j) key[j] = 0;
+        if (vid < C * nv && owner >= 0) {
+          const int slice = owner / kBeamThreads, t = owner % kBeamThreads;
+          const int vec = slice * kBeamThreads * nv + (vid % nv) * kBeamThreads + t;
+          if (vec < r.nvec) {
+            const int e0 = r.head + vec * U;
+            float y[U];
+            load_vector<E>(y, x + e0);
+#pragma unroll
+            for (int j = 0; j < U; ++j) key[j] = beam_key(y[j], (uint32_t)(e0 + j));
+          }
+          if (vid % nv == 0 && slice == 0) {
+            const int e = beam_extra<E>(r, V, t);
+            if (e >= 0) key[U] = beam_key(load_logit(x + e), (uint32_t)e);
+          }
+        }
+        // wanted: better than the last of the list, and not in it already
+        bool wanted = false;
+#pragma unroll
+        for (int j = 0; j <= U; ++j) {
+          if (key[j] <= least) key[j] = 0;
+          wanted |= key[j] != 0;
+        }
+        if (!__any(wanted)) continue;
+        for (int c = 0; c < C; ++c) {
+          const uint64_t have = __shfl((unsigned long long)list, c);
+#pragma unroll
+          for (int j = 0; j <= U; ++j)
+            if (key[j] == have) key[j] = 0;
+        }
+        uint64_t keep = 0;
+        before = ~0ull;
+        for (int c = 0; c < C; ++c) {
+          uint64_t b = list < before ? list : 0;
+#pragma unroll
+          for (int j = 0; j <= U; ++j)
+            if (key[j] < before && key[j] > b) b = key[j];
+          b = wave_max(b);
+          if (lane == c) keep = b;
+          before = b;
+          if (b == 0) break;
+        }
+        list = keep;
+        least = __shfl((unsigned long long)list, C - 1);
+      }
+      const float v = key_value(list);
+      if (v > -INFINITY) mine = (double)score + ((double)v - lse);
+      at = (uint64_t)k << 32 | key_at(list);
     }
-    const float v = key_value(list);
-    mine.score = v > -INFINITY ? (double)score + ((double)v - lse) : -INFINITY;
-    mine.at = (uint64_t)k * V + key_at(list);
+    if (!(mine == mine)) mine = -INFINITY;  // a score that is not a number
+    if (lane < C) {
+      cand_score[k * C + lane] = mine;
+      cand_at[k * C + lane] = at;
+    }
+    if (lane == 0) done[k] = fin;
   }
-  if (lane < C) cand[k * C + lane] = mine;
   __syncthreads();
   if (k != 0) return;
-  // the K best of the K x C candidates (C = K, or V < K candidates a row)
+  // the K best of the K x C candidates (C = K, or V < K candidates a row):
+  // the largest score, then the lowest index with it
   constexpr int CL = kBeamMax * kBeamMax / 64;
-  BeamCandidate own[CL];
+  uint64_t sk[CL], ak[CL];
 #pragma unroll
   for (int i = 0; i < CL; ++i) {
-    own[i].score = -INFINITY;
-    own[i].at = ~0ull;
-    if (lane + 64 * i < K * C) own[i] = cand[lane + 64 * i];
-    if (!(own[i].score == own[i].score)) own[i].score = -INFINITY;  // a score that is not a number
+    sk[i] = ak[i] = 0;
+    if (lane + 64 * i < K * C) {
+      sk[i] = double_key(cand_score[lane + 64 * i]);
+      ak[i] = ~cand_at[lane + 64 * i];
+    }
   }
-  BeamCandidate prev = {INFINITY, 0};
-  bool any = false;
   for (int c = 0; c < K; ++c) {
-    BeamCandidate b = {-INFINITY, ~0ull};
+    uint64_t s = 0, t = 0;
+#pragma unroll
+    for (int i = 0; i < CL; ++i) s = sk[i] > s ? sk[i] : s;
+    s = wave_max(s);
+#pragma unroll
+    for (int i = 0; i < CL; ++i) t = sk[i] == s && ak[i] > t ? ak[i] : t;
+    t = wave_max(t);
 #pragma unroll
     for (int i = 0; i < CL; ++i)
-      if ((!any || better(prev, own[i])) && better(own[i], b)) b = own[i];
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) {
-      BeamCandidate o;
-      o.score = __shfl_xor(b.score, m);
-      o.at = __shfl_xor((unsigned long long)b.at, m);
-      if (better(o, b)) b = o;
-    }
-    prev = b;
-    any = true;
+      if (ak[i] == t) sk[i] = ak[i] = 0;
     if (lane == 0) {
-      // (V K >= K candidates always exist; the guard keeps a wrong one in range)
-      const uint64_t at = b.at < (uint64_t)K * V ? b.at : 0;
-      const int parent = (int)(at / V), token = (int)(at % V);
+      // (K V >= K candidates always exist; the clamps keep a wrong one in range)
+      const int parent = min((int)(~t >> 32 & 0xffffu), K - 1);
+      const int token = min((uint32_t)~t, (uint32_t)(V - 1));
       const int64_t o = (int64_t)g * K + c;
-      a.out_scores[o] = (float)b.score;
+      a.out_scores[o] = (float)key_double(s);
       a.out_tokens[o] = token;
       a.out_parents[o] = parent;
       if (a.out_finished) a.out_finished[o] = done[parent] || token == a.end_token;
