@@ -85,6 +85,31 @@ __device__ __forceinline__ int64_t slot_of(int n, int64_t bos, int seg, int64_t 
   return bos / seg + 2 * (int64_t)n + j;
 }
 
+// Sequence of rank r when the sequences are ordered longest first (ties by
+// index), so that the longest walks start first.  Every thread of the
+// workgroup calls it.  Up to 256 sequences; more keep their order.
+constexpr int kRankedSeqs = 256;
+template <int THREADS>
+__device__ __forceinline__ int longest_first(int* lds, const int32_t* cu, int N, int64_t T, int r) {
+  if (!cu || N == 1 || N > kRankedSeqs) return r;
+  for (int i = threadIdx.x; i < N; i += THREADS) {
+    int64_t bos, eos;
+    seq_range(cu, i, T, bos, eos);
+    lds[i] = (int)(eos - bos);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += THREADS) {
+    const int mine = lds[i];
+    int rank = 0;
+    for (int m = 0; m < N; ++m) rank += lds[m] > mine || (lds[m] == mine && m < i);
+    if (rank == r) lds[kRankedSeqs] = i;
+  }
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(lds[kRankedSeqs]);
+  __syncthreads();  // the LDS is used for tiles from here on
+  return n;
+}
+
 // ---- LDS tiles ------------------------------------------------------------
 // A tile holds C tokens x W channels, row-major, its 16-byte units XOR-ed
 // with a function of the row so that what one instruction reads falls on
@@ -296,31 +321,41 @@ __device__ __forceinline__ double suffix_sum(double x, int lane) {
 }
 
 // NW compute waves of 16 value columns each: 4 (half a head) or 8 (a head).
-// Chunks of 64 tokens for half heads, 32 for whole ones (half of that in
-// fp32), so that a query or key tile is 16 or 8 KiB.
-template <typename E, int NW, bool DG>
+// Chunks of 64 tokens (32 in fp32), query and key tiles of three chunks and
+// value tiles of two in LDS.  The dk walk that forms the decays' gradient (DK),
+// whose pair waves also need the values and x, takes chunks of half that
+// length, four in LDS, and so does the dq walk before it (DG): what r_t counts
+// as coming through the state is what the dk walk does not count as a pair.
+template <typename E, int NW, bool DG, bool DK>
 struct WalkLayout {
   static constexpr int ES = (int)sizeof(E);
-  static constexpr int C = (NW == 4 ? 128 : 64) / ES;
+  static constexpr int C = (DG ? 64 : 128) / ES;
   static constexpr int TILE = C * D * ES;              // a query, key or x tile
   static constexpr int VW = 16 * NW;                   // value columns of the workgroup
   static constexpr int VTILE = C * VW * ES;
   static constexpr int K = TILE, V = 2 * TILE, X = V + VTILE;
-  static constexpr int SET = X + (DG ? TILE : 0);      // the tiles of a chunk
-  static constexpr int NBUF = NW == 4 ? 3 : DG ? 4 : 5;  // chunks in LDS
-  static constexpr int COPIES = SET / 1024;            // copy instructions per chunk
+  static constexpr int SET = DK ? X + TILE : 2 * TILE; // tiles that arrive together
+  static constexpr int NBUF = DK ? 4 : 3;
+  static constexpr int VALS = NBUF * SET;              // [2] value tiles (not DK)
+  static constexpr int COPIES = SET / 1024;            // copy instructions per set
   static constexpr int RB = C * ES;                    // bytes of a pair matrix row
-  static constexpr int PAIR = NBUF * SET;              // E [2][C][C]
+  static constexpr int PAIR = VALS + (DK ? 0 : 2 * VTILE);  // E [2][C][C]
   static constexpr int SUM = PAIR + 2 * C * RB;        // float [4][2][C] prefix sums (log2), high and low part
   static constexpr int ROW = SUM + 4 * 2 * C * 4;      // float [4][C] factor of the state in row t
   static constexpr int WGT = ROW + 4 * C * 4;          // float [4][C] factor of token t in the state
   static constexpr int GAM = WGT + 4 * C * 4;          // float [4] factor of the state over the chunk
   static constexpr int ANC = GAM + 16;                 // float [4][NW] <S, dS> by compute wave
-  static constexpr int RX = ANC + 16 * NW;             // float [4][NW][C] state part . x by compute wave
-  static constexpr int RR = RX + (DG ? 4 * NW * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
-  static constexpr int RC = RR + (DG ? 8 * C * 4 : 0);       // float [4][C] pair sums of the queries
-  static constexpr int BYTES = RC + (DG ? 4 * C * 4 : 0);
+  static constexpr int RX = ANC + 16 * NW;             // float [2][NW][C] state part . x by compute wave
+  static constexpr int RR = RX + (DG ? 2 * NW * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
+  static constexpr int RC = RR + (DK ? 8 * C * 4 : 0);       // float [4][C] pair sums of the queries
+  static constexpr int BYTES = RC + (DK ? 4 * C * 4 : 0);
 };
+
+// The state is kept as 2^s times what the accumulators hold, so that a chunk's
+// decay need not scale them: the decay wave moves it into s, and with it into
+// the factors of rows and tokens, until s falls below this (the factors stay
+// below 2^30) or the state itself is wanted.
+constexpr double kScaleFloor = -30.0;
 
 // ---------------------------------------------------------------------------
 // The walk.  NW + 4 waves per (sequence or segment, head, block of 16 NW value
@@ -336,29 +371,27 @@ struct WalkLayout {
 //              products with the keys up to them scaled by e^{G_i - G_j}
 //   a decay wave: prefix sums and factors of chunk c + 2; with DG the decays'
 //              gradient of chunk c - 1
-//   a loader:  copies tiles from global memory straight into LDS, up to
-//              NBUF - 1 chunks ahead of the compute waves, which therefore
-//              never wait behind a copy of their own
-// A wave issues at most one matrix product per 16 cycles and one vector
-// instruction per 4, half of what its SIMD can do (measured), and a compute
-// wave is bound by that; so a whole head takes eight waves of 16 columns
-// rather than four of 32 (where they measured 1.9 times as long per chunk),
-// and half a head, whose four waves have a SIMD each, takes longer chunks,
-// which need fewer instructions per token.
+//   a loader:  copies tiles from global memory straight into LDS, queries and
+//              keys two chunks ahead of the compute waves, values one
+// A compute wave is bound by instructions, not by the matrix cores (a wave
+// issues at most one vector instruction in 4 cycles, and a product holds it
+// for 12 more): a whole head takes eight waves of 16 columns rather than four
+// of 32, chunks are as long as LDS allows, and what can be is left to the
+// other waves.
 // REV walks backwards in time: the pair matrix is upper triangular and the
 // factors of rows and of tokens change places.
 // DG (the decays' gradient): x is q in the dq walk and k in the dk walk.
 // ---------------------------------------------------------------------------
 template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
-  using L = WalkLayout<E, NW, DG>;
+  constexpr bool DK = DG && REV;               // dk walk: forms the decays' gradient
+  using L = WalkLayout<E, NW, DG, DK>;
   using TF = typename Tok<E>::F;
   constexpr int TN = Tok<E>::N;
   constexpr int C = L::C, NT = C / 16, ES = L::ES, NBUF = L::NBUF;
   constexpr bool BF = ES == 2;
   constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values
   constexpr int NSS = (BF && DG) ? 3 : 1;      // terms of the state in the outputs' product
-  constexpr bool DK = DG && REV;               // dk walk: forms the decays' gradient
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
   constexpr int KT = C / (4 * TN);             // token steps per chunk
   constexpr int TPS = NT / KT;                 // 16-token tiles per token step
@@ -405,9 +438,9 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     if constexpr (!OUT)
       if (REV ? first : last) return;  // no segment follows that would read it
   } else {
-    n = (int)rank;
+    n = longest_first<64 * (NW + 4)>(reinterpret_cast<int*>(smem), p.cu, p.num_seqs, p.total_tokens, (int)rank);
     seq_range(p.cu, n, p.total_tokens, bos, eos);
-    slot = slot_of(n, bos, p.seg, 0);
+    slot = 0;
     tb = bos;
     te = eos;
     first = last = true;
@@ -415,20 +448,27 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   const int nch = (int)((te - tb + C - 1) / C);
   const size_t nh = (size_t)n * H + h;
   auto chunk_of = [&](int ci) { return REV ? nch - 1 - ci : ci; };
-  auto tiles = [&](int ci) { return smem + (ci % NBUF) * L::SET; };
+  // whether the state behind chunk ci (in the walk's order) is at a boundary
+  // where the decays' gradient takes it from memory or leaves it there
+  auto at_anchor = [&](int ci) {
+    const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+    return ((REV ? t0 : t0 + C) - bos) % p.anchor == 0;
+  };
   // Iteration ci (from -1): compute waves on chunk ci, pair waves on ci + 1,
-  // decay wave on ci + 2 and back on ci - 1, loader on ci + NBUF - 1.
+  // decay wave on ci + 2 and back on ci - 1.
 
   if (wv == NW + 3) {
     // ---- loader ----
     // 1 KiB pieces, 16 bytes a lane; the lanes' offsets are the same in every
     // chunk.  Rows behind the end lie outside the buffer view and arrive as
     // zeros.
-    auto copy_tile = [&](auto width, const void* src, int heads, int ch0, int64_t t0, int nv, unsigned char* dst) {
+    auto copy_tile = [&](auto width, const void* src, int heads, int ch0, int ci, unsigned char* dst) {
       constexpr int W = decltype(width)::value;
       constexpr int NPC = C * W * ES / 1024;   // pieces
       constexpr int UR = W * ES / 16;          // 16-byte units per row
       constexpr int RP = 64 / UR;              // rows per piece
+      const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+      const int nv = (int)min((int64_t)C, te - t0);
       const uint32_t stride = (uint32_t)heads * (D * ES);
       const char* base = static_cast<const char*>(src) + ((size_t)t0 * heads + h / (H / heads)) * (D * ES);
       const Rsrc rs = make_rsrc(base, (uint32_t)(nv - 1) * stride + D * ES);
@@ -441,25 +481,36 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         row += RP * stride;
       }
     };
-    auto copy_chunk = [&](int ci) {
-      const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
-      const int nv = (int)min((int64_t)C, te - t0);
-      unsigned char* dst = tiles(ci);
-      using Whole = std::integral_constant<int, D>;
-      using Block = std::integral_constant<int, L::VW>;
-      if (OUT) copy_tile(Whole{}, p.q, p.q_heads, 0, t0, nv, dst);
-      copy_tile(Whole{}, p.k, p.k_heads, 0, t0, nv, dst + L::K);
-      copy_tile(Block{}, p.v, p.v_heads, cb * L::VW, t0, nv, dst + L::V);
-      if constexpr (DG) copy_tile(Whole{}, p.x, p.x_heads, 0, t0, nv, dst + L::X);
+    using Whole = std::integral_constant<int, D>;
+    using Block = std::integral_constant<int, L::VW>;
+    auto copy_set = [&](int ci) {
+      if (ci >= nch) return;
+      unsigned char* dst = smem + (ci % NBUF) * L::SET;
+      if (OUT) copy_tile(Whole{}, p.q, p.q_heads, 0, ci, dst);
+      copy_tile(Whole{}, p.k, p.k_heads, 0, ci, dst + L::K);
+      if constexpr (DK) {
+        copy_tile(Whole{}, p.v, p.v_heads, 0, ci, dst + L::V);
+        copy_tile(Whole{}, p.x, p.x_heads, 0, ci, dst + L::X);
+      }
     };
-    constexpr int PER = L::COPIES - (OUT ? 0 : L::TILE / 1024);  // copies per chunk
-    for (int ci = 0; ci < NBUF - 1 && ci < nch; ++ci) copy_chunk(ci);
-    for (int ci = -1; ci < nch; ++ci) {
-      // chunk ci + 1 has landed; the ones behind it may be in flight
-      if (ci + NBUF - 2 < nch) __builtin_amdgcn_s_waitcnt(vmcnt_wait((NBUF - 3) * PER < 63 ? (NBUF - 3) * PER : 63));
-      else __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
-      chunk_barrier();
-      if (ci >= 0 && ci + NBUF - 1 < nch) copy_chunk(ci + NBUF - 1);
+    if constexpr (DK) {
+      for (int ci = 0; ci < NBUF - 1; ++ci) copy_set(ci);
+      for (int ci = -1; ci < nch; ++ci) {
+        // chunk ci + 1 has landed; the one behind it may be in flight
+        if (ci + NBUF - 2 < nch) __builtin_amdgcn_s_waitcnt(vmcnt_wait((NBUF - 3) * L::COPIES));
+        else __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+        chunk_barrier();
+        if (ci >= 0) copy_set(ci + NBUF - 1);
+      }
+    } else {
+      copy_set(0);
+      for (int ci = -1; ci < nch; ++ci) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+        chunk_barrier();
+        copy_set(ci + 2);
+        if (ci + 1 < nch)
+          copy_tile(Block{}, p.v, p.v_heads, cb * L::VW, ci + 1, smem + L::VALS + ((ci + 1) & 1) * L::VTILE);
+      }
     }
     if constexpr (DG) chunk_barrier();
     return;
@@ -480,21 +531,30 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       return lane < C && tb + (int64_t)chunk_of(ci) * C + lane < te ? la_head : 0.f;
     };
     double log_total = 0.0;
+    double scale = 0.0;  // s: the state is 2^s times the accumulators
     auto put_decay = [&](int ci, float la) {
       const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
       const double s = prefix_sum<C>((double)fmaxf(la, kMinLogDecay) * kLog2e, lane);
       const double tot = read_lane(s, C - 1);
       log_total += tot;
-      const float head = exp2_fast((float)s), tail = exp2_fast((float)(tot - s));
+      const double before = scale;
+      scale += tot;
+      float gam = 1.f;
+      if (scale < kScaleFloor || ci == nch - 1 || (DG && at_anchor(ci))) {
+        gam = exp2_fast((float)scale);
+        scale = 0.0;
+      }
+      const float row = exp2_fast((float)(before + (REV ? tot - s : s)));
+      const float wgt = exp2_fast((float)((REV ? s : tot - s) - scale));
       const int b = ci & 3;
       if (lane < C) {
         const float hi = (float)s;
         sSum[b * 2 * C + lane] = hi;
         sSum[b * 2 * C + C + lane] = (float)(s - (double)hi);
-        sRow[b * C + lane] = REV ? tail : head;
-        sWgt[b * C + lane] = t < te ? (REV ? head : tail) : 0.f;
+        sRow[b * C + lane] = row;
+        sWgt[b * C + lane] = t < te ? wgt : 0.f;
       }
-      if (lane == 0) sGam[b] = exp2_fast((float)tot);
+      if (lane == 0) sGam[b] = gam;
     };
     // the decays' gradient of a chunk from the other waves' sums
     double flow = 0.0;   // D behind the chunk
@@ -506,7 +566,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       float part = 0.f;
       if (lane < C)
 #pragma unroll
-        for (int w = 0; w < NW; ++w) part += sRX[(b * NW + w) * C + lane];
+        for (int w = 0; w < NW; ++w) part += sRX[((ci & 1) * NW + w) * C + lane];
       if constexpr (!REV) {
         if (in) p.row_dot[(size_t)(t0 + lane) * H + h] = part;
       } else {
@@ -517,8 +577,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
           queries = sRC[b * C + lane];
         }
         const int64_t tend = min(te, t0 + C);
-        if (tend == te || (tend - bos) % p.seg == 0)
-        {
+        if (tend == te || (tend - bos) % p.anchor == 0) {
           flow = 0.0;
 #pragma unroll
           for (int w = 0; w < NW; ++w) flow += (double)sAnc[b * NW + w];
@@ -561,94 +620,125 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 
   if (wv >= NW) {
     // ---- pair matrix of chunk ci + 1, keys in rows: lane = query, four consecutive keys ----
-    // wave p takes the query tiles p and NT - 1 - p, one from each end of the triangle
-    const int pw = wv - NW;
     const uint32_t k_at = tile_at<E, D>(l16, 8 * g);
-    for (int ci = -1; ci < nch; ++ci) {
-      chunk_barrier();
-      if (!OUT || pw >= NT || ci + 1 >= nch) continue;
-      const uint32_t base = (uint32_t)((ci + 1) % NBUF) * L::SET;
-      unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * L::RB);
-      const int b = (ci + 1) & 3;
-      const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
-      const int nv = (int)min((int64_t)C, te - t0);
-      const float* gs = sSum + b * 2 * C;
-      f32x4 rsum[DK ? NT : 1];
+    // query tiles RA and RB (RB < 0: none) by pair wave PW
+    auto pairs = [&](auto pw_, auto ra_, auto rb_) {
+      constexpr int PW = decltype(pw_)::value, RA = decltype(ra_)::value, RBT = decltype(rb_)::value;
+      constexpr int ROWS = RBT >= 0 ? 2 : 1;
+      (void)PW;
+      for (int ci = -1; ci < nch; ++ci) {
+        chunk_barrier();
+        if (!OUT || ci + 1 >= nch) continue;
+        const uint32_t base = (uint32_t)((ci + 1) % NBUF) * L::SET;
+        unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * L::RB);
+        const int b = (ci + 1) & 3;
+        const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
+        const int nv = (int)min((int64_t)C, te - t0);
+        const float* gs = sSum + b * 2 * C;
+        Frag<E> fq[ROWS][4], fx[DK ? ROWS : 1][DK ? 4 : 1];
 #pragma unroll
-      for (int kt = 0; kt < (DK ? NT : 1); ++kt) rsum[kt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < ROWS; ++r) {
+          constexpr int rts[2] = {RA, RBT};
 #pragma unroll
-      for (int half = 0; half < (NT == 4 ? 2 : 1); ++half) {
-        const int rt = half ? NT - 1 - pw : pw;
-        const int q = 16 * rt + l16;
-        Frag<E> fq[4];
+          for (int ks = 0; ks < 4; ++ks) ld_row(fq[r][ks], smem, base + k_at + 16 * rts[r] * (D * ES), 32 * ks);
+          if constexpr (DK)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) ld_row(fq[ks], smem, base + k_at + 16 * rt * (D * ES), 32 * ks);
-        Frag<E> fx[DK ? 4 : 1];
-        if constexpr (DK)
+            for (int ks = 0; ks < 4; ++ks) ld_row(fx[r][ks], smem, base + L::X + k_at + 16 * rts[r] * (D * ES), 32 * ks);
+        }
+        float gq[ROWS], gq_lo[ROWS], csum[ROWS];
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) ld_row(fx[ks], smem, base + L::X + k_at + 16 * rt * (D * ES), 32 * ks);
-        const float gq = gs[q], gq_lo = gs[C + q];
-        float csum = 0.f;
+        for (int r = 0; r < ROWS; ++r) {
+          constexpr int rts[2] = {RA, RBT};
+          gq[r] = gs[16 * rts[r] + l16];
+          gq_lo[r] = gs[C + 16 * rts[r] + l16];
+          csum[r] = 0.f;
+        }
 #pragma unroll
         for (int kt = 0; kt < NT; ++kt) {
-          const bool tri = REV ? kt >= rt : kt <= rt;
-          // a tile beyond the triangle that shares a token step with it is zero
-          if (!tri && kt / TPS != rt / TPS) continue;
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          if (tri) {
-            f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
+          constexpr int rts[2] = {RA, RBT};
+          Frag<E> fk[4], fv[DK ? 4 : 1];
+          bool any = false;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              Frag<E> fk;
-              ld_row(fk, smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
-              acc = mma(acc, fk, fq[ks]);
-            }
+          for (int r = 0; r < ROWS; ++r) any |= REV ? kt >= rts[r] : kt <= rts[r];
+          f32x4 gk, gk_lo, rsum = {0.f, 0.f, 0.f, 0.f};
+          if (any) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) ld_row(fk[ks], smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
             if constexpr (DK)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                Frag<E> fv;
-                ld_row(fv, smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
-                acc2 = mma(acc2, fv, fx[ks]);
-              }
-            const f32x4 gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
-            const f32x4 gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 16 * kt + 4 * g + i;
-              const bool on = REV ? (k >= q && k < nv) : k <= q;
-              const float d = (gq - gk[i]) + (gq_lo - gk_lo[i]);
-              const float e = acc[i] * exp2_fast(REV ? -d : d);
-              const float x = on ? e : 0.f;
-              if constexpr (DK) {
-                const float f = (on && k != q) ? x * acc2[i] : 0.f;
-                rsum[kt][i] += f;
-                csum += f;
-              }
-              acc[i] = x;
-            }
+              for (int ks = 0; ks < 4; ++ks) ld_row(fv[ks], smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
+            gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
+            gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
           }
-          const uint32_t at = BF ? pair_at<L::RB>(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at<L::RB>(q, 4 * kt + g);
-          store_row4(reinterpret_cast<E*>(pair + at), acc);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const int rt = rts[r];
+            const bool tri = REV ? kt >= rt : kt <= rt;
+            // a tile beyond the triangle that shares a token step with it is zero
+            if (!tri && kt / TPS != rt / TPS) continue;
+            const int q = 16 * rt + l16;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            if (tri) {
+              f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) acc = mma(acc, fk[ks], fq[r][ks]);
+              if constexpr (DK)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) acc2 = mma(acc2, fv[ks], fx[r][ks]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 16 * kt + 4 * g + i;
+                // (keys behind the end are zeros; backwards, so are their factors' uses)
+                const bool on = kt != rt || (REV ? k >= q : k <= q);
+                const float d = (gq[r] - gk[i]) + (gq_lo[r] - gk_lo[i]);
+                const float e = acc[i] * exp2_fast(REV ? -d : d);
+                const float x = on && (!REV || k < nv) ? e : 0.f;
+                if constexpr (DK) {
+                  const float f = (on && k != q && k < nv) ? x * acc2[i] : 0.f;
+                  rsum[i] += f;
+                  csum[r] += f;
+                }
+                acc[i] = x;
+              }
+            }
+            const uint32_t at = BF ? pair_at<L::RB>(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at<L::RB>(q, 4 * kt + g);
+            store_row4(reinterpret_cast<E*>(pair + at), acc);
+          }
+          if constexpr (DK) {
+            // over the 16 queries of the tiles
+#pragma unroll
+            for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) rsum[i] += __shfl_xor(rsum[i], m);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + PW) * C + 16 * kt + 4 * g) = rsum;
+          }
         }
         if constexpr (DK) {
-          csum += __shfl_xor(csum, 16);
-          csum += __shfl_xor(csum, 32);
-          if (g == 0) sRC[b * C + q] = csum;
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            constexpr int rts[2] = {RA, RBT};
+            csum[r] += __shfl_xor(csum[r], 16);
+            csum[r] += __shfl_xor(csum[r], 32);
+            if (g == 0) sRC[b * C + 16 * rts[r] + l16] = csum[r];
+          }
         }
       }
-      if constexpr (DK) {
-        // over the 16 queries of a tile
-#pragma unroll
-        for (int kt = 0; kt < NT; ++kt) {
-#pragma unroll
-          for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rsum[kt][i] += __shfl_xor(rsum[kt][i], m);
-          if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + pw) * C + 16 * kt + 4 * g) = rsum[kt];
-        }
-      }
+      if constexpr (DG) chunk_barrier();
+    };
+    // one tile from each end of the triangle
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using None = std::integral_constant<int, -1>;
+    if (wv == NW) {
+      if constexpr (NT == 4) pairs(I0{}, I0{}, std::integral_constant<int, 3>{});
+      else pairs(I0{}, I0{}, None{});
+    } else if constexpr (NT == 1) {
+      for (int ci = -1; ci < nch; ++ci) chunk_barrier();
+      if constexpr (DG) chunk_barrier();
+    } else {
+      if constexpr (NT == 4) pairs(I1{}, I1{}, std::integral_constant<int, 2>{});
+      else pairs(I1{}, I1{}, None{});
     }
-    if constexpr (DG) chunk_barrier();
     return;
   }
 
@@ -682,6 +772,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     }
   };
   constexpr size_t kState = (size_t)D * D;
+  // the state at the boundary of the sequence's stretch j of `anchor` tokens
+  auto anchor_state = [&](int64_t j) {
+    return p.fwd_snap + ((size_t)slot_of(n, bos, p.anchor, j) * H + h) * kState;
+  };
   f32x4 accS[8];
   {
     const float* src = nullptr;
@@ -702,40 +796,59 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   uint32_t k_at[Tok<E>::READS], v_at[Tok<E>::READS];
   col_at<D>(k_at, static_cast<const E*>(nullptr), 0, l16, g);
   col_at<L::VW>(v_at, static_cast<const E*>(nullptr), vc0, l16, g);
-  const uint32_t q_at = tile_at<E, D>(l16, 4 * g), x_at = tile_at<E, D>(l16, col0 + 4 * g);
+  const uint32_t q_at = tile_at<E, D>(l16, 4 * g);
   uint32_t p_at[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) p_at[kt] = pair_at<L::RB>(l16, 4 * kt + g);
   const int oes = TR && p.o_f32 ? 4 : ES;
   const uint32_t o_row = (uint32_t)H * (D * oes);
   const uint32_t o_at = (uint32_t)l16 * o_row + (uint32_t)((col0 + 4 * g) * oes);
-  Frag<E> fq[OUT ? 4 : 1][NT];
-  auto read_q = [&](uint32_t at) {
+  // queries of the channel steps ks and ks + 1 are held at a time
+  Frag<E> fq[OUT ? 2 : 1][NT];
+  auto read_q = [&](uint32_t at, int ks) {
+    if constexpr (OUT)
 #pragma unroll
-    for (int ks = 0; ks < (OUT ? 4 : 0); ++ks)
-#pragma unroll
-      for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks][rt], smem, at + q_at, 32 * ks, 16 * rt);
+      for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks & 1][rt], smem, at + q_at, 32 * ks, 16 * rt);
   };
+  // x of a chunk's rows, in the layout of the outputs (dq walk: from memory, a
+  // chunk ahead; the dk walk has it in LDS)
+  using Raw = std::conditional_t<BF, u32x2, f32x4>;
+  Raw xr[DG && !REV ? NT : 1];
+  auto load_x = [&](int ci) {
+    if constexpr (DG && !REV) {
+      const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+      const int nv = (int)min((int64_t)C, te - t0);
+      const uint32_t stride = (uint32_t)p.x_heads * (D * ES);
+      const Rsrc rs = make_rsrc(static_cast<const char*>(p.x) + ((size_t)t0 * p.x_heads + h / (H / p.x_heads)) * (D * ES),
+                                ci < nch ? (uint32_t)(nv - 1) * stride + D * ES : 0);
+#pragma unroll
+      for (int rt = 0; rt < NT; ++rt) {
+        const int off = (int)((16 * rt + l16) * stride + (col0 + 4 * g) * ES);
+        if constexpr (BF) xr[rt] = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+        else xr[rt] = __builtin_bit_cast(f32x4, buf_ld16(rs, (uint32_t)off, 0));
+      }
+    }
+  };
+  load_x(0);
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
-  uint32_t base = 0;  // of the chunk's tiles
-  read_q(base);
+  uint32_t base = 0;  // of the chunk's query and key tiles
+  read_q(base, 0);
+  read_q(base, 1);
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
     const int b = ci & 3;
 
-    // what the decays' gradient needs of the states at segment boundaries
+    // what the decays' gradient needs of the states at boundaries
     if constexpr (DG && !REV) {
-      if (!p.segmented && (t0 - bos) % p.seg == 0)
-        store_state(p.fwd_snap + ((size_t)(slot + (t0 - bos) / p.seg) * H + h) * kState, accS);
+      if (p.fwd_snap != p.snap && (t0 - bos) % p.anchor == 0) store_state(anchor_state((t0 - bos) / p.anchor), accS);
     }
     if constexpr (DK) {
       const int64_t tend = t0 + nv;
-      if (tend == te || (tend - bos) % p.seg == 0) {
-        const int64_t sl = slot_of(n, bos, p.seg, (tend - bos + p.seg - 1) / p.seg);
+      if (tend == te || (tend - bos) % p.anchor == 0) {
         f32x4 x[8];
-        load_state(p.fwd_snap + ((size_t)sl * H + h) * kState, x);
+        load_state(anchor_state((tend - bos + p.anchor - 1) / p.anchor), x);
         float dot = 0.f;
 #pragma unroll
         for (int rt = 0; rt < 8; ++rt)
@@ -752,6 +865,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     // use (at most 15 can be waited for one by one); the vector arithmetic
     // fills the gaps between products.
     const uint32_t base_next = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
+    const uint32_t vbase = DK ? base + L::V : L::VALS + (ci & 1) * L::VTILE;
     const float gam = sGam[b];
     float w[KT][TN];
     TF fv[KT], fk[8];
@@ -763,7 +877,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
       }
-      ld_col(fv[kt], smem, base + L::V + kt * (4 * TN * L::VW * ES), v_at, 0);
+      ld_col(fv[kt], smem, vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
     }
     auto read_k = [&](int kt, int first, int count) {
 #pragma unroll
@@ -805,14 +919,12 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 #pragma unroll
         for (int s = 0; s < NSS; ++s)
 #pragma unroll
-          for (int rt = 0; rt < NT; ++rt) accO[rt] = mma(accO[rt], fs[s], fq[ks][rt]);
-        accS[2 * ks] *= gam;
-        accS[2 * ks + 1] *= gam;
-        if (ks >= 2) read_k(0, 2 * (ks - 2), 2);
+          for (int rt = 0; rt < NT; ++rt) accO[rt] = mma(accO[rt], fs[s], fq[ks & 1][rt]);
+        if (ks < 2) read_q(base, ks + 2);
+        else read_k(0, 2 * (ks - 2), 2);
         __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) weigh_values(kt);
+      weigh_values(0);
       TF fp[NT][KT];
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt)
@@ -828,15 +940,19 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         if constexpr (DG) {
           float dot = 0.f;
           Frag16<E> fx;
-          ld_frag16(fx, reinterpret_cast<const E*>(smem + base + L::X + x_at + 16 * rt * (D * ES)));
+          if constexpr (REV)
+            ld_frag16(fx, reinterpret_cast<const E*>(smem + base + L::X + tile_at<E, D>(l16, col0 + 4 * g) + 16 * rt * (D * ES)));
+          else
+            fx.v = __builtin_bit_cast(decltype(fx.v), xr[rt]);
           const f32x4 x = frag16_to_f32(fx);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dot += x[i] * accO[rt][i];
           dot += __shfl_xor(dot, 16);
           dot += __shfl_xor(dot, 32);
-          if (g == 0) sRX[(b * NW + wv) * C + 16 * rt + l16] = dot;
+          if (g == 0) sRX[((ci & 1) * NW + wv) * C + 16 * rt + l16] = dot;
         }
       }
+      load_x(ci + 1);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -844,15 +960,18 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
           if (REV ? kt >= rt / TPS : kt <= rt / TPS) accO[rt] = mma_tok(accO[rt], fv[kt], fp[rt][kt]);
     } else {
       read_k(0, 0, 8);
+      weigh_values(0);
+    }
+    // the state's scale, when the decays have run far enough (decay wave)
+    if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gam)) != 0x3f800000) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt) accS[rt] *= gam;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) weigh_values(kt);
     }
     // state, with the outputs' stores in between
     add_to_state(0);
     if constexpr (KT == 2) {
       read_k(1, 0, 8);
+      weigh_values(1);
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (OUT) {
@@ -874,15 +993,15 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     if constexpr (KT == 2) add_to_state(1);
     // the next chunk's queries: its tiles are in LDS already (the last chunk
     // reads what is there and drops it)
-    read_q(base_next);
+    read_q(base_next, 0);
+    read_q(base_next, 1);
     base = base_next;
   }
   if constexpr (DG) chunk_barrier();  // the last chunk's sums
   if (OUT) {
     if (p.fin && (REV ? first : last)) store_state(p.fin + nh * kState, accS);
     if constexpr (DG && !REV)
-      if (last && nch > 0)
-        store_state(p.fwd_snap + ((size_t)slot_of(n, bos, p.seg, (eos - bos + p.seg - 1) / p.seg) * H + h) * kState, accS);
+      if (last && nch > 0) store_state(anchor_state((eos - bos + p.anchor - 1) / p.anchor), accS);
   } else {
     store_state(p.snap + ((size_t)slot * H + h) * kState, accS);
   }
@@ -890,7 +1009,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 
 template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
 hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
-  using L = WalkLayout<E, NW, DG>;
+  using L = WalkLayout<E, NW, DG, DG && REV>;
   constexpr int CB = 8 / NW;
   const int64_t blocks = (a.units + 7) / 8 * 8 * CB;
   static std::atomic<bool> set[64];

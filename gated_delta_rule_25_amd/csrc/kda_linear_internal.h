@@ -53,7 +53,9 @@ struct LinearWalkArgs {
   void* o;                 // [T, H, 128] in the I/O dtype, or fp32 (o_f32)
   bool o_f32;
   // gradient of the decays
-  float* fwd_snap;         // [slots][H][128,128]: S entering each segment, and behind the last one
+  int anchor;              // tokens between the boundaries at which it is taken from the states (a multiple of 64)
+  float* fwd_snap;         // [slots by `anchor`][H][128,128]: S at every boundary, and behind the last token
+                           // (`snap` itself when segments are of that length)
   float* row_dot;          // [T, H]: q_t . dq_t's part through the state (dq walk writes, dk walk reads)
   float* d_log_decay;      // [T, H] or null (dk walk)
   double* d_decay_part;    // decay_per_head: [work items] sums (dk walk), else null
