@@ -140,29 +140,37 @@ template <typename E, int W>
 __device__ __forceinline__ uint32_t tile_at(int row, int ch) {
   return (uint32_t)(row * W * (int)sizeof(E) + ((ch * (int)sizeof(E)) ^ (swizzle<E, W>(row) << 4)));
 }
+// Reads at a byte address of LDS (a number rather than a pointer, so that the
+// XORs are on it and its constant parts stay in the instruction).
 template <typename T>
-__device__ __forceinline__ T lds_get(const unsigned char* smem, uint32_t at) {
-  return *reinterpret_cast<const T*>(smem + at);
+__device__ __forceinline__ T lds_get(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
+}
+// The same for 8-byte halves of an operand: volatile, or two rows' halves are
+// fetched by one instruction into registers that moves have to sort again.
+template <typename T>
+__device__ __forceinline__ T lds_get_half(uint32_t at) {
+  return *reinterpret_cast<const volatile __attribute__((address_space(3))) T*>(at);
 }
 
 // operand with the channels ch .. ch+7 of a row; `at` = the lane's 8 g, ch0 = 32 ks
-__device__ __forceinline__ void ld_row(Frag<__bf16>& f, const unsigned char* m, uint32_t at, int ch0) {
-  f.v = lds_get<bf16x8>(m, at ^ (uint32_t)(ch0 * 2));
+__device__ __forceinline__ void ld_row(Frag<__bf16>& f, uint32_t at, int ch0) {
+  f.v = lds_get<bf16x8>(at ^ (uint32_t)(ch0 * 2));
 }
-__device__ __forceinline__ void ld_row(Frag<float>& f, const unsigned char* m, uint32_t at, int ch0) {
-  f.lo = lds_get<f32x4>(m, at ^ (uint32_t)(ch0 * 4));
-  f.hi = lds_get<f32x4>(m, at ^ (uint32_t)(ch0 * 4 + 16));
+__device__ __forceinline__ void ld_row(Frag<float>& f, uint32_t at, int ch0) {
+  f.lo = lds_get<f32x4>(at ^ (uint32_t)(ch0 * 4));
+  f.hi = lds_get<f32x4>(at ^ (uint32_t)(ch0 * 4 + 16));
 }
 // operand with the channels ch0 + 4 g .. and ch0 + 16 + 4 g .. of a row (what
 // two stacked accumulator tiles hold); `at` = the lane's 4 g
-__device__ __forceinline__ void ld_row_acc(Frag<__bf16>& f, const unsigned char* m, uint32_t at, int ch0, int rows) {
-  const bf16x4 a = lds_get<bf16x4>(m, (at ^ (uint32_t)(ch0 * 2)) + rows * (D * 2));
-  const bf16x4 b = lds_get<bf16x4>(m, (at ^ (uint32_t)(ch0 * 2 + 32)) + rows * (D * 2));
-  f.v = (bf16x8){a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+__device__ __forceinline__ void ld_row_acc(Frag<__bf16>& f, uint32_t at, int ch0, int rows) {
+  const u32x2 a = lds_get_half<u32x2>((at ^ (uint32_t)(ch0 * 2)) + rows * (D * 2));
+  const u32x2 b = lds_get_half<u32x2>((at ^ (uint32_t)(ch0 * 2 + 32)) + rows * (D * 2));
+  f.v = __builtin_bit_cast(bf16x8, (u32x4){a[0], a[1], b[0], b[1]});
 }
-__device__ __forceinline__ void ld_row_acc(Frag<float>& f, const unsigned char* m, uint32_t at, int ch0, int rows) {
-  f.lo = lds_get<f32x4>(m, (at ^ (uint32_t)(ch0 * 4)) + rows * (D * 4));
-  f.hi = lds_get<f32x4>(m, (at ^ (uint32_t)(ch0 * 4 + 64)) + rows * (D * 4));
+__device__ __forceinline__ void ld_row_acc(Frag<float>& f, uint32_t at, int ch0, int rows) {
+  f.lo = lds_get<f32x4>((at ^ (uint32_t)(ch0 * 4)) + rows * (D * 4));
+  f.hi = lds_get<f32x4>((at ^ (uint32_t)(ch0 * 4 + 64)) + rows * (D * 4));
 }
 
 // Operands whose contraction runs over a chunk's tokens: 32 deep in bf16
@@ -202,16 +210,16 @@ __device__ __forceinline__ void col_at(uint32_t (&at)[4], const float*, int ch, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) at[i] = tile_at<float, W>(4 * g + i, ch + l16);
 }
-__device__ __forceinline__ void ld_col(Frag<__bf16>& f, unsigned char* m, uint32_t base, const uint32_t (&at)[2], int ch0) {
+__device__ __forceinline__ void ld_col(Frag<__bf16>& f, uint32_t base, const uint32_t (&at)[2], int ch0) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(m + ((base + at[0]) ^ (uint32_t)(ch0 * 2))));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(m + ((base + at[1]) ^ (uint32_t)(ch0 * 2))));
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)((base + at[0]) ^ (uint32_t)(ch0 * 2)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)((base + at[1]) ^ (uint32_t)(ch0 * 2)));
   const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
   f.v = (bf16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 }
-__device__ __forceinline__ void ld_col(Frag16<float>& f, unsigned char* m, uint32_t base, const uint32_t (&at)[4], int ch0) {
+__device__ __forceinline__ void ld_col(Frag16<float>& f, uint32_t base, const uint32_t (&at)[4], int ch0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>(m, (base + at[i]) ^ (uint32_t)(ch0 * 4));
+  for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>((base + at[i]) ^ (uint32_t)(ch0 * 4));
 }
 // The pair matrix: rows of RB = 64 or 128 bytes, their 16-byte units XOR-ed so
 // that the rows of a 16-byte read (above) fall on all banks.  pair_at: the
@@ -224,8 +232,8 @@ __device__ __forceinline__ uint32_t pair_at(int row, int u) {
   return (uint32_t)(row * RB + ((u ^ x) << 4));
 }
 // a row over the lane's tokens (unit g)
-__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<bf16x8>(m, at); }
-__device__ __forceinline__ void ld_pair(Frag16<float>& f, const unsigned char* m, uint32_t at) { f.v = lds_get<f32x4>(m, at); }
+__device__ __forceinline__ void ld_pair(Frag<__bf16>& f, uint32_t at) { f.v = lds_get<bf16x8>(at); }
+__device__ __forceinline__ void ld_pair(Frag16<float>& f, uint32_t at) { f.v = lds_get<f32x4>(at); }
 __device__ __forceinline__ float frag_get(const Frag<__bf16>& f, int i) { return (float)f.v[i]; }
 __device__ __forceinline__ float frag_get(const Frag16<float>& f, int i) { return f.v[i]; }
 
@@ -395,7 +403,8 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
   constexpr int KT = C / (4 * TN);             // token steps per chunk
   constexpr int TPS = NT / KT;                 // 16-token tiles per token step
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
   float* sSum = reinterpret_cast<float*>(smem + L::SUM);
   float* sRow = reinterpret_cast<float*>(smem + L::ROW);
   float* sWgt = reinterpret_cast<float*>(smem + L::WGT);
@@ -462,16 +471,25 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     // 1 KiB pieces, 16 bytes a lane; the lanes' offsets are the same in every
     // chunk.  Rows behind the end lie outside the buffer view and arrive as
     // zeros.
-    auto copy_tile = [&](auto width, const void* src, int heads, int ch0, int ci, unsigned char* dst) {
+    // the tensors from this head's rows on
+    struct Rows {
+      const char* base;
+      uint32_t stride;
+    };
+    auto rows_of = [&](const void* src, int heads) {
+      return Rows{static_cast<const char*>(src) + (size_t)(h / (H / heads)) * (D * ES), (uint32_t)heads * (D * ES)};
+    };
+    const Rows rq = rows_of(p.q, p.q_heads), rk = rows_of(p.k, p.k_heads), rv = rows_of(p.v, p.v_heads);
+    const Rows rx = DK ? rows_of(p.x, p.x_heads) : rq;
+    auto copy_tile = [&](auto width, const Rows& src, int ch0, int ci, unsigned char* dst) {
       constexpr int W = decltype(width)::value;
       constexpr int NPC = C * W * ES / 1024;   // pieces
       constexpr int UR = W * ES / 16;          // 16-byte units per row
       constexpr int RP = 64 / UR;              // rows per piece
       const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
       const int nv = (int)min((int64_t)C, te - t0);
-      const uint32_t stride = (uint32_t)heads * (D * ES);
-      const char* base = static_cast<const char*>(src) + ((size_t)t0 * heads + h / (H / heads)) * (D * ES);
-      const Rsrc rs = make_rsrc(base, (uint32_t)(nv - 1) * stride + D * ES);
+      const uint32_t stride = src.stride;
+      const Rsrc rs = make_rsrc(src.base + (size_t)t0 * stride, (uint32_t)(nv - 1) * stride + D * ES);
       uint32_t row = (uint32_t)(lane / UR) * stride + ch0 * ES;
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
@@ -486,11 +504,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     auto copy_set = [&](int ci) {
       if (ci >= nch) return;
       unsigned char* dst = smem + (ci % NBUF) * L::SET;
-      if (OUT) copy_tile(Whole{}, p.q, p.q_heads, 0, ci, dst);
-      copy_tile(Whole{}, p.k, p.k_heads, 0, ci, dst + L::K);
+      if (OUT) copy_tile(Whole{}, rq, 0, ci, dst);
+      copy_tile(Whole{}, rk, 0, ci, dst + L::K);
       if constexpr (DK) {
-        copy_tile(Whole{}, p.v, p.v_heads, 0, ci, dst + L::V);
-        copy_tile(Whole{}, p.x, p.x_heads, 0, ci, dst + L::X);
+        copy_tile(Whole{}, rv, 0, ci, dst + L::V);
+        copy_tile(Whole{}, rx, 0, ci, dst + L::X);
       }
     };
     if constexpr (DK) {
@@ -509,7 +527,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         chunk_barrier();
         copy_set(ci + 2);
         if (ci + 1 < nch)
-          copy_tile(Block{}, p.v, p.v_heads, cb * L::VW, ci + 1, smem + L::VALS + ((ci + 1) & 1) * L::VTILE);
+          copy_tile(Block{}, rv, cb * L::VW, ci + 1, smem + L::VALS + ((ci + 1) & 1) * L::VTILE);
       }
     }
     if constexpr (DG) chunk_barrier();
@@ -629,7 +647,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       for (int ci = -1; ci < nch; ++ci) {
         chunk_barrier();
         if (!OUT || ci + 1 >= nch) continue;
-        const uint32_t base = (uint32_t)((ci + 1) % NBUF) * L::SET;
+        const uint32_t base = lds0 + (uint32_t)((ci + 1) % NBUF) * L::SET;
         unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * L::RB);
         const int b = (ci + 1) & 3;
         const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
@@ -640,10 +658,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         for (int r = 0; r < ROWS; ++r) {
           constexpr int rts[2] = {RA, RBT};
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) ld_row(fq[r][ks], smem, base + k_at + 16 * rts[r] * (D * ES), 32 * ks);
+          for (int ks = 0; ks < 4; ++ks) ld_row(fq[r][ks], base + k_at + 16 * rts[r] * (D * ES), 32 * ks);
           if constexpr (DK)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) ld_row(fx[r][ks], smem, base + L::X + k_at + 16 * rts[r] * (D * ES), 32 * ks);
+            for (int ks = 0; ks < 4; ++ks) ld_row(fx[r][ks], base + L::X + k_at + 16 * rts[r] * (D * ES), 32 * ks);
         }
         float gq[ROWS], gq_lo[ROWS], csum[ROWS];
 #pragma unroll
@@ -663,10 +681,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
           f32x4 gk, gk_lo, rsum = {0.f, 0.f, 0.f, 0.f};
           if (any) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) ld_row(fk[ks], smem, base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
+            for (int ks = 0; ks < 4; ++ks) ld_row(fk[ks], base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
             if constexpr (DK)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) ld_row(fv[ks], smem, base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
+              for (int ks = 0; ks < 4; ++ks) ld_row(fv[ks], base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
             gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
             gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
           }
@@ -808,7 +826,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   auto read_q = [&](uint32_t at, int ks) {
     if constexpr (OUT)
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks & 1][rt], smem, at + q_at, 32 * ks, 16 * rt);
+      for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks & 1][rt], at + q_at, 32 * ks, 16 * rt);
   };
   // x of a chunk's rows, in the layout of the outputs (dq walk: from memory, a
   // chunk ahead; the dk walk has it in LDS)
@@ -832,7 +850,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   load_x(0);
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
-  uint32_t base = 0;  // of the chunk's query and key tiles
+  uint32_t base = lds0;  // of the chunk's query and key tiles
   read_q(base, 0);
   read_q(base, 1);
   for (int ci = 0; ci < nch; ++ci) {
@@ -864,8 +882,8 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     // The LDS reads run a few operands ahead of the products, in the order of
     // use (at most 15 can be waited for one by one); the vector arithmetic
     // fills the gaps between products.
-    const uint32_t base_next = base + L::SET == NBUF * L::SET ? 0 : base + L::SET;
-    const uint32_t vbase = DK ? base + L::V : L::VALS + (ci & 1) * L::VTILE;
+    const uint32_t base_next = base + L::SET == lds0 + NBUF * L::SET ? lds0 : base + L::SET;
+    const uint32_t vbase = DK ? base + L::V : lds0 + L::VALS + (ci & 1) * L::VTILE;
     const float gam = sGam[b];
     float w[KT][TN];
     TF fv[KT], fk[8];
@@ -877,12 +895,12 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
       }
-      ld_col(fv[kt], smem, vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
+      ld_col(fv[kt], vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
     }
     auto read_k = [&](int kt, int first, int count) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt)
-        if (rt >= first && rt < first + count) ld_col(fk[rt], smem, base + L::K + kt * (4 * TN * D * ES), k_at, 16 * rt);
+        if (rt >= first && rt < first + count) ld_col(fk[rt], base + L::K + kt * (4 * TN * D * ES), k_at, 16 * rt);
     };
     // values times their factors, in the terms of the state's update
     TF fw[KT][NSV];
@@ -931,7 +949,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
           if (REV ? kt >= rt / TPS : kt <= rt / TPS)
-            ld_pair(fp[rt][kt], smem, L::PAIR + (ci & 1) * (C * L::RB) + p_at[kt] + 16 * rt * L::RB);
+            ld_pair(fp[rt][kt], lds0 + L::PAIR + (ci & 1) * (C * L::RB) + p_at[kt] + 16 * rt * L::RB);
       read_k(0, 4, 4);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -941,7 +959,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
           float dot = 0.f;
           Frag16<E> fx;
           if constexpr (REV)
-            ld_frag16(fx, reinterpret_cast<const E*>(smem + base + L::X + tile_at<E, D>(l16, col0 + 4 * g) + 16 * rt * (D * ES)));
+            ld_frag16(fx, reinterpret_cast<const E*>(smem + (base - lds0) + L::X + tile_at<E, D>(l16, col0 + 4 * g) + 16 * rt * (D * ES)));
           else
             fx.v = __builtin_bit_cast(decltype(fx.v), xr[rt]);
           const f32x4 x = frag16_to_f32(fx);
