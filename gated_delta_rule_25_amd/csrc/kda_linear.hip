@@ -466,6 +466,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   // Iteration ci (from -1): compute waves on chunk ci, pair waves on ci + 1,
   // decay wave on ci + 2 and back on ci - 1.
 
+  // The SIMDs serve their oldest wave first; what the compute waves wait for
+  // at the next barrier goes ahead of them.
+  if (wv >= NW) __builtin_amdgcn_s_setprio(2);
+
   if (wv == NW + 3) {
     // ---- loader ----
     // 1 KiB pieces, 16 bytes a lane; the lanes' offsets are the same in every
