@@ -17,9 +17,10 @@
 // loss flows through a_t S_{t-1}, and that changes from token to token by
 //   D_t = D_{t+1} + r_t - c_t,  r_t = q_t . dq_t,  c_t = k_t . dk_t
 // (each without the token's own q_t . k_t term, which cancels), and at any
-// token boundary equals <S, dS>.  The sum over t is restarted from that
-// product at every segment boundary, so rounding cannot build up along the
-// sequence.
+// token boundary equals <S, dS>.  The dq walk leaves the r_t and the dk walk
+// the c_t, and both the states at every boundary of `anchor` tokens; the sum
+// over t is restarted from their product there, so that rounding cannot build
+// up along the sequence (linear_decay_grad_kernel).
 //
 // What is rounded.  bf16: the pair matrix (q_i . k_j) e^{..} and the state,
 // as operands of the outputs' products, to one bf16 each (the output is bf16
@@ -221,6 +222,14 @@ __device__ __forceinline__ void ld_col(Frag16<float>& f, uint32_t base, const ui
 #pragma unroll
   for (int i = 0; i < 4; ++i) f.v[i] = lds_get<float>((base + at[i]) ^ (uint32_t)(ch0 * 4));
 }
+// the same from memory (raw buffer view, byte offset)
+__device__ __forceinline__ void buf_row(Frag<__bf16>& f, const Rsrc& rs, uint32_t off) {
+  f.v = __builtin_bit_cast(bf16x8, buf_ld16(rs, off, 0));
+}
+__device__ __forceinline__ void buf_row(Frag<float>& f, const Rsrc& rs, uint32_t off) {
+  f.lo = __builtin_bit_cast(f32x4, buf_ld16(rs, off, 0));
+  f.hi = __builtin_bit_cast(f32x4, buf_ld16(rs, off, 16));
+}
 // The pair matrix: rows of RB = 64 or 128 bytes, their 16-byte units XOR-ed so
 // that the rows of a 16-byte read (above) fall on all banks.  pair_at: the
 // byte offset of unit u; the tokens of step kt are the units 4 kt ...
@@ -292,11 +301,47 @@ __device__ __forceinline__ double dpp_move(double x) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp_move_f32(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ double read_lane(double x, int l) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sums over the lanes of a column (lane mod 16): of four values at a time, each
+// row of 16 lanes ending with one of them (`tile` says which), or of two, every
+// other row ending with one (tile -1: none).
+__device__ __forceinline__ float swap_add32(float a, float b) {  // lower half: a's, upper half: b's sums of halves
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                  false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
+__device__ __forceinline__ float swap_add16(float a, float b) {  // even rows: a's, odd rows: b's sums of row pairs
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                  false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
+__device__ __forceinline__ float sum_groups(const float (&x)[4], int g, int& tile) {
+  tile = (g & 1) << 1 | g >> 1;
+  return swap_add16(swap_add32(x[0], x[1]), swap_add32(x[2], x[3]));
+}
+__device__ __forceinline__ float sum_groups(const float (&x)[2], int g, int& tile) {
+  const float s = swap_add32(x[0], x[1]);
+  tile = g & 1 ? -1 : g >> 1;
+  return swap_add16(s, s);
+}
+// Sum over the 16 lanes of a row, in every one of them.
+__device__ __forceinline__ float sum_row(float x) {
+  x += dpp_move_f32<0x128>(x);
+  x += dpp_move_f32<0x124>(x);
+  x += dpp_move_f32<0x122>(x);
+  x += dpp_move_f32<0x121>(x);
+  return x;
 }
 // Sums over the lanes 0 .. lane (prefix) and lane .. C - 1 (suffix) of C lanes.
 template <int C>
@@ -330,33 +375,29 @@ __device__ __forceinline__ double suffix_sum(double x, int lane) {
 
 // NW compute waves of 16 value columns each: 4 (half a head) or 8 (a head).
 // Chunks of 64 tokens (32 in fp32), query and key tiles of three chunks and
-// value tiles of two in LDS.  The dk walk that forms the decays' gradient (DK),
-// whose pair waves also need the values and x, takes chunks of half that
-// length, four in LDS, and so does the dq walk before it (DG): what r_t counts
-// as coming through the state is what the dk walk does not count as a pair.
+// value tiles of two in LDS.  All walks take the same chunks: what r_t counts
+// as coming through the state (dq walk) is what the dk walk (DK) does not
+// count as a pair.
 template <typename E, int NW, bool DG, bool DK>
 struct WalkLayout {
   static constexpr int ES = (int)sizeof(E);
-  static constexpr int C = (DG ? 64 : 128) / ES;
-  static constexpr int TILE = C * D * ES;              // a query, key or x tile
+  static constexpr int C = 128 / ES;
+  static constexpr int TILE = C * D * ES;              // a query or key tile
   static constexpr int VW = 16 * NW;                   // value columns of the workgroup
   static constexpr int VTILE = C * VW * ES;
-  static constexpr int K = TILE, V = 2 * TILE, X = V + VTILE;
-  static constexpr int SET = DK ? X + TILE : 2 * TILE; // tiles that arrive together
-  static constexpr int NBUF = DK ? 4 : 3;
-  static constexpr int VALS = NBUF * SET;              // [2] value tiles (not DK)
-  static constexpr int COPIES = SET / 1024;            // copy instructions per set
+  static constexpr int K = TILE, SET = 2 * TILE;       // tiles that arrive together
+  static constexpr int NBUF = 3;
+  static constexpr int VALS = NBUF * SET;              // [2] value tiles
   static constexpr int RB = C * ES;                    // bytes of a pair matrix row
-  static constexpr int PAIR = VALS + (DK ? 0 : 2 * VTILE);  // E [2][C][C]
+  static constexpr int PAIR = VALS + 2 * VTILE;        // E [2][C][C]
   static constexpr int SUM = PAIR + 2 * C * RB;        // float [4][2][C] prefix sums (log2), high and low part
   static constexpr int ROW = SUM + 4 * 2 * C * 4;      // float [4][C] factor of the state in row t
   static constexpr int WGT = ROW + 4 * C * 4;          // float [4][C] factor of token t in the state
   static constexpr int GAM = WGT + 4 * C * 4;          // float [4] factor of the state over the chunk
-  static constexpr int ANC = GAM + 16;                 // float [4][NW] <S, dS> by compute wave
-  static constexpr int RX = ANC + 16 * NW;             // float [2][NW][C] state part . x by compute wave
-  static constexpr int RR = RX + (DG ? 2 * NW * C * 4 : 0);  // float [4][2][C] pair sums of the keys by pair wave
-  static constexpr int RC = RR + (DK ? 8 * C * 4 : 0);       // float [4][C] pair sums of the queries
-  static constexpr int BYTES = RC + (DK ? 4 * C * 4 : 0);
+  static constexpr int RX = GAM + 16;                  // float [2][NW][C] state part . x by compute wave
+  static constexpr int RR = RX + (DG ? 2 * NW * C * 4 : 0);  // float [2][2][C] pair sums of the keys by pair wave
+  static constexpr int RC = RR + (DK ? 4 * C * 4 : 0);       // float [2][C] pair sums of the queries
+  static constexpr int BYTES = RC + (DK ? 2 * C * 4 : 0);
 };
 
 // The state is kept as 2^s times what the accumulators hold, so that a chunk's
@@ -391,7 +432,7 @@ constexpr double kScaleFloor = -30.0;
 // DG (the decays' gradient): x is q in the dq walk and k in the dk walk.
 // ---------------------------------------------------------------------------
 template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
-__global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
+__device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* smem, int64_t u, int cb) {
   constexpr bool DK = DG && REV;               // dk walk: forms the decays' gradient
   using L = WalkLayout<E, NW, DG, DK>;
   using TF = typename Tok<E>::F;
@@ -403,25 +444,17 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
   constexpr int KT = C / (4 * TN);             // token steps per chunk
   constexpr int TPS = NT / KT;                 // 16-token tiles per token step
-  extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
   float* sSum = reinterpret_cast<float*>(smem + L::SUM);
   float* sRow = reinterpret_cast<float*>(smem + L::ROW);
   float* sWgt = reinterpret_cast<float*>(smem + L::WGT);
   float* sGam = reinterpret_cast<float*>(smem + L::GAM);
-  float* sAnc = reinterpret_cast<float*>(smem + L::ANC);
   float* sRX = reinterpret_cast<float*>(smem + L::RX);
   float* sRR = reinterpret_cast<float*>(smem + L::RR);
   float* sRC = reinterpret_cast<float*>(smem + L::RC);
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int CB = 8 / NW;  // column blocks of a head
-  // blocks b and b + 8 run on the same XCD: a head's column blocks share its L2
-  const int64_t slot8 = blockIdx.x >> 3;
-  const int cb = (int)(slot8 % CB);
-  const int64_t u = (slot8 / CB) * 8 + (blockIdx.x & 7);
-  if (u >= p.units) return;
   const int H = p.num_heads;
   const int h = (int)(u % H);
   const int64_t rank = u / H;
@@ -431,11 +464,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   bool first, last;  // the item begins / ends its sequence
   if (p.segmented) {
     const Segment s = find_segment(p.cu, p.num_seqs, p.total_tokens, p.seg, rank);
-    if (!s.ok) {
-      if constexpr (DK)
-        if (p.d_decay_part && tid == 0) p.d_decay_part[u] = 0.0;
-      return;
-    }
+    if (!s.ok) return;
     n = s.n;
     bos = s.bos;
     eos = s.eos;
@@ -484,7 +513,6 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       return Rows{static_cast<const char*>(src) + (size_t)(h / (H / heads)) * (D * ES), (uint32_t)heads * (D * ES)};
     };
     const Rows rq = rows_of(p.q, p.q_heads), rk = rows_of(p.k, p.k_heads), rv = rows_of(p.v, p.v_heads);
-    const Rows rx = DK ? rows_of(p.x, p.x_heads) : rq;
     auto copy_tile = [&](auto width, const Rows& src, int ch0, int ci, unsigned char* dst) {
       constexpr int W = decltype(width)::value;
       constexpr int NPC = C * W * ES / 1024;   // pieces
@@ -510,29 +538,14 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       unsigned char* dst = smem + (ci % NBUF) * L::SET;
       if (OUT) copy_tile(Whole{}, rq, 0, ci, dst);
       copy_tile(Whole{}, rk, 0, ci, dst + L::K);
-      if constexpr (DK) {
-        copy_tile(Whole{}, rv, 0, ci, dst + L::V);
-        copy_tile(Whole{}, rx, 0, ci, dst + L::X);
-      }
     };
-    if constexpr (DK) {
-      for (int ci = 0; ci < NBUF - 1; ++ci) copy_set(ci);
-      for (int ci = -1; ci < nch; ++ci) {
-        // chunk ci + 1 has landed; the one behind it may be in flight
-        if (ci + NBUF - 2 < nch) __builtin_amdgcn_s_waitcnt(vmcnt_wait((NBUF - 3) * L::COPIES));
-        else __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
-        chunk_barrier();
-        if (ci >= 0) copy_set(ci + NBUF - 1);
-      }
-    } else {
-      copy_set(0);
-      for (int ci = -1; ci < nch; ++ci) {
-        __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
-        chunk_barrier();
-        copy_set(ci + 2);
-        if (ci + 1 < nch)
-          copy_tile(Block{}, rv, cb * L::VW, ci + 1, smem + L::VALS + ((ci + 1) & 1) * L::VTILE);
-      }
+    copy_set(0);
+    for (int ci = -1; ci < nch; ++ci) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+      chunk_barrier();
+      copy_set(ci + 2);
+      if (ci + 1 < nch)
+        copy_tile(Block{}, rv, cb * L::VW, ci + 1, smem + L::VALS + ((ci + 1) & 1) * L::VTILE);
     }
     if constexpr (DG) chunk_barrier();
     return;
@@ -578,63 +591,35 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       }
       if (lane == 0) sGam[b] = gam;
     };
-    // the decays' gradient of a chunk from the other waves' sums
-    double flow = 0.0;   // D behind the chunk
-    double dsum = 0.0;
-    auto finish = [&](int ci, float rdot) {
+    // what this walk's columns say of the decays' gradient at a chunk's tokens
+    auto finish = [&](int ci) {
       const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
-      const bool in = lane < C && t0 + lane < te;
-      const int b = ci & 3;
+      if (lane >= C || t0 + lane >= te) return;
       float part = 0.f;
-      if (lane < C)
 #pragma unroll
-        for (int w = 0; w < NW; ++w) part += sRX[((ci & 1) * NW + w) * C + lane];
-      if constexpr (!REV) {
-        if (in) p.row_dot[(size_t)(t0 + lane) * H + h] = part;
-      } else {
-        float keys = 0.f, queries = 0.f;
-        if (lane < C) {
+      for (int w = 0; w < NW; ++w) part += sRX[((ci & 1) * NW + w) * C + lane];
+      if constexpr (DK) {
+        // pairs within the chunk, as queries (c) and as keys (r)
+        part += sRC[(ci & 1) * C + lane];
 #pragma unroll
-          for (int w = 0; w < (NT > 1 ? 2 : 1); ++w) keys += sRR[(b * 2 + w) * C + lane];
-          queries = sRC[b * C + lane];
-        }
-        const int64_t tend = min(te, t0 + C);
-        if (tend == te || (tend - bos) % p.anchor == 0) {
-          flow = 0.0;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) flow += (double)sAnc[b * NW + w];
-        }
-        const double s = suffix_sum<C>(in ? ((double)rdot + (double)keys) - ((double)part + (double)queries) : 0.0, lane);
-        const double d = flow + s;
-        if (in) {
-          if (p.d_log_decay) p.d_log_decay[(size_t)(t0 + lane) * H + h] = (float)d;
-          dsum += d;
-        }
-        flow += read_lane(s, 0);
+        for (int w = 0; w < 2; ++w) part -= sRR[((ci & 1) * 2 + w) * C + lane];
       }
+      p.change[((size_t)cb * H + h) * p.total_tokens + t0 + lane] = part;
     };
     if (nch > 0) put_decay(0, load_decay(0));
     // two iterations ahead of their use, one in flight over a barrier
-    float la_next = load_decay(1), rdot_next = 0.f;
+    float la_next = load_decay(1);
     for (int ci = -1; ci < nch; ++ci) {
       chunk_barrier();
-      const float la = la_next, rdot = rdot_next;
+      const float la = la_next;
       la_next = load_decay(ci + 3);
-      if constexpr (DK) rdot_next = load_rows(p.row_dot, ci);
       if (ci + 2 < nch) put_decay(ci + 2, la);
       if constexpr (DG)
-        if (ci > 0) finish(ci - 1, rdot);
+        if (ci > 0) finish(ci - 1);
     }
     if constexpr (DG) {
       chunk_barrier();
-      if (nch > 0) finish(nch - 1, rdot_next);
-      if constexpr (REV) {
-        if (p.d_decay_part) {
-#pragma unroll
-          for (int m = 32; m >= 1; m >>= 1) dsum += __shfl_xor(dsum, m);
-          if (lane == 0) p.d_decay_part[u] = dsum;
-        }
-      }
+      if (nch > 0) finish(nch - 1);
     }
     if (!OUT && lane == 0 && cb == 0) p.seg_decay[(size_t)slot * H + h] = exp2_fast((float)log_total);
     return;
@@ -648,8 +633,77 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       constexpr int PW = decltype(pw_)::value, RA = decltype(ra_)::value, RBT = decltype(rb_)::value;
       constexpr int ROWS = RBT >= 0 ? 2 : 1;
       (void)PW;
+      constexpr int rts[2] = {RA, RBT};
+      auto in_triangle = [](int kt, int rt) { return REV ? kt >= rt : kt <= rt; };
+      // DK: a chunk later, when its values have come, the pairs' products with
+      // (v . x) over the block's columns, summed by query and by key.  x comes
+      // from memory a chunk ahead.
+      constexpr int XS = L::VW / 32;
+      Frag<E> fx[DK ? ROWS : 1][DK ? XS : 1];
+      f32x4 held[DK ? ROWS : 1][DK ? NT : 1];
+      const uint32_t v_at = tile_at<E, L::VW>(l16, 8 * g);
+      auto fetch_x = [&](int ci) {
+        if constexpr (DK) {
+          const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
+          const int nv = (int)min((int64_t)C, te - t0);
+          const uint32_t stride = (uint32_t)p.x_heads * (D * ES);
+          const Rsrc rs = make_rsrc(static_cast<const char*>(p.x) + ((size_t)t0 * p.x_heads + h / (H / p.x_heads)) * (D * ES),
+                                    ci < nch ? (uint32_t)(nv - 1) * stride + D * ES : 0);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int ks = 0; ks < XS; ++ks)
+              buf_row(fx[r][ks], rs, (uint32_t)(16 * rts[r] + l16) * stride + (cb * L::VW + 32 * ks + 8 * g) * ES);
+        }
+      };
+      auto sum_pairs = [&](int ci) {
+        if constexpr (DK) {
+          const uint32_t vbase = lds0 + L::VALS + (ci & 1) * L::VTILE + v_at;
+          const int nv = (int)min((int64_t)C, te - (tb + (int64_t)chunk_of(ci) * C));
+          float csum[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) csum[r] = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < NT; ++kt) {
+            f32x4 rsum = {0.f, 0.f, 0.f, 0.f};
+            Frag<E> fv[XS];
+#pragma unroll
+            for (int ks = 0; ks < XS; ++ks) ld_row(fv[ks], vbase + 16 * kt * (L::VW * ES), 32 * ks);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+              if (!in_triangle(kt, rts[r])) continue;
+              f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int ks = 0; ks < XS; ++ks) acc = mma(acc, fv[ks], fx[r][ks]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 16 * kt + 4 * g + i, q = 16 * rts[r] + l16;
+                // (the token's own pair cancels)
+                const float f = k > q && k < nv ? held[r][kt][i] * acc[i] : 0.f;
+                rsum[i] += f;
+                csum[r] += f;
+              }
+            }
+            // over the 16 queries of the tiles
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rsum[i] = sum_row(rsum[i]);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + ((ci & 1) * 2 + PW) * C + 16 * kt + 4 * g) = rsum;
+          }
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            csum[r] = swap_add32(csum[r], csum[r]);
+            csum[r] = swap_add16(csum[r], csum[r]);
+            if (g == 0) sRC[(ci & 1) * C + 16 * rts[r] + l16] = csum[r];
+          }
+        }
+      };
+      if (DK && nch > 0) fetch_x(0);
       for (int ci = -1; ci < nch; ++ci) {
         chunk_barrier();
+        if (DK && ci >= 0) {
+          sum_pairs(ci);
+          fetch_x(ci + 1);
+        }
         if (!OUT || ci + 1 >= nch) continue;
         const uint32_t base = lds0 + (uint32_t)((ci + 1) % NBUF) * L::SET;
         unsigned char* pair = smem + L::PAIR + ((ci + 1) & 1) * (C * L::RB);
@@ -657,91 +711,49 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         const int64_t t0 = tb + (int64_t)chunk_of(ci + 1) * C;
         const int nv = (int)min((int64_t)C, te - t0);
         const float* gs = sSum + b * 2 * C;
-        Frag<E> fq[ROWS][4], fx[DK ? ROWS : 1][DK ? 4 : 1];
+        Frag<E> fq[ROWS][4];
+        float gq[ROWS], gq_lo[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          constexpr int rts[2] = {RA, RBT};
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) ld_row(fq[r][ks], base + k_at + 16 * rts[r] * (D * ES), 32 * ks);
-          if constexpr (DK)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) ld_row(fx[r][ks], base + L::X + k_at + 16 * rts[r] * (D * ES), 32 * ks);
-        }
-        float gq[ROWS], gq_lo[ROWS], csum[ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          constexpr int rts[2] = {RA, RBT};
           gq[r] = gs[16 * rts[r] + l16];
           gq_lo[r] = gs[C + 16 * rts[r] + l16];
-          csum[r] = 0.f;
         }
 #pragma unroll
         for (int kt = 0; kt < NT; ++kt) {
-          constexpr int rts[2] = {RA, RBT};
-          Frag<E> fk[4], fv[DK ? 4 : 1];
-          bool any = false;
-#pragma unroll
-          for (int r = 0; r < ROWS; ++r) any |= REV ? kt >= rts[r] : kt <= rts[r];
-          f32x4 gk, gk_lo, rsum = {0.f, 0.f, 0.f, 0.f};
-          if (any) {
+          Frag<E> fk[4];
+          f32x4 gk, gk_lo;
+          if (in_triangle(kt, RA) || (ROWS > 1 && in_triangle(kt, RBT))) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) ld_row(fk[ks], base + L::K + k_at + 16 * kt * (D * ES), 32 * ks);
-            if constexpr (DK)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks) ld_row(fv[ks], base + L::V + k_at + 16 * kt * (D * ES), 32 * ks);
             gk = *reinterpret_cast<const f32x4*>(gs + 16 * kt + 4 * g);
             gk_lo = *reinterpret_cast<const f32x4*>(gs + C + 16 * kt + 4 * g);
           }
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
             const int rt = rts[r];
-            const bool tri = REV ? kt >= rt : kt <= rt;
+            const bool tri = in_triangle(kt, rt);
             // a tile beyond the triangle that shares a token step with it is zero
             if (!tri && kt / TPS != rt / TPS) continue;
             const int q = 16 * rt + l16;
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
             if (tri) {
-              f32x4 acc2 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks) acc = mma(acc, fk[ks], fq[r][ks]);
-              if constexpr (DK)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) acc2 = mma(acc2, fv[ks], fx[r][ks]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int k = 16 * kt + 4 * g + i;
                 // (keys behind the end are zeros; backwards, so are their factors' uses)
                 const bool on = kt != rt || (REV ? k >= q : k <= q);
                 const float d = (gq[r] - gk[i]) + (gq_lo[r] - gk_lo[i]);
-                const float e = acc[i] * exp2_fast(REV ? -d : d);
-                const float x = on && (!REV || k < nv) ? e : 0.f;
-                if constexpr (DK) {
-                  const float f = (on && k != q && k < nv) ? x * acc2[i] : 0.f;
-                  rsum[i] += f;
-                  csum[r] += f;
-                }
-                acc[i] = x;
+                const float x = acc[i] * exp2_fast(REV ? -d : d);
+                acc[i] = on && (!REV || k < nv) ? x : 0.f;
               }
+              if constexpr (DK) held[r][kt] = acc;
             }
             const uint32_t at = BF ? pair_at<L::RB>(q, 2 * kt + (g >> 1)) + 8 * (g & 1) : pair_at<L::RB>(q, 4 * kt + g);
             store_row4(reinterpret_cast<E*>(pair + at), acc);
-          }
-          if constexpr (DK) {
-            // over the 16 queries of the tiles
-#pragma unroll
-            for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) rsum[i] += __shfl_xor(rsum[i], m);
-            if (l16 == 0) *reinterpret_cast<f32x4*>(sRR + (b * 2 + PW) * C + 16 * kt + 4 * g) = rsum;
-          }
-        }
-        if constexpr (DK) {
-#pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            constexpr int rts[2] = {RA, RBT};
-            csum[r] += __shfl_xor(csum[r], 16);
-            csum[r] += __shfl_xor(csum[r], 32);
-            if (g == 0) sRC[b * C + 16 * rts[r] + l16] = csum[r];
           }
         }
       }
@@ -754,9 +766,6 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     if (wv == NW) {
       if constexpr (NT == 4) pairs(I0{}, I0{}, std::integral_constant<int, 3>{});
       else pairs(I0{}, I0{}, None{});
-    } else if constexpr (NT == 1) {
-      for (int ci = -1; ci < nch; ++ci) chunk_barrier();
-      if constexpr (DG) chunk_barrier();
     } else {
       if constexpr (NT == 4) pairs(I1{}, I1{}, std::integral_constant<int, 2>{});
       else pairs(I1{}, I1{}, None{});
@@ -794,9 +803,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     }
   };
   constexpr size_t kState = (size_t)D * D;
-  // the state at the boundary of the sequence's stretch j of `anchor` tokens
-  auto anchor_state = [&](int64_t j) {
-    return p.fwd_snap + ((size_t)slot_of(n, bos, p.anchor, j) * H + h) * kState;
+  // what the decays' gradient needs of the state: S entering stretch j of
+  // `anchor` tokens (dq walk), dS behind it (dk walk)
+  auto leave_state = [&](int64_t j, const f32x4 (&s)[8]) {
+    store_state(p.anchors + ((size_t)slot_of(n, bos, p.anchor, j) * H + h) * kState, s);
   };
   f32x4 accS[8];
   {
@@ -832,12 +842,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) ld_row_acc(fq[ks & 1][rt], at + q_at, 32 * ks, 16 * rt);
   };
-  // x of a chunk's rows, in the layout of the outputs (dq walk: from memory, a
-  // chunk ahead; the dk walk has it in LDS)
+  // x of a chunk's rows, in the layout of the outputs, from memory a chunk ahead
   using Raw = std::conditional_t<BF, u32x2, f32x4>;
-  Raw xr[DG && !REV ? NT : 1];
+  Raw xr[DG ? NT : 1];
   auto load_x = [&](int ci) {
-    if constexpr (DG && !REV) {
+    if constexpr (DG) {
       const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
       const int nv = (int)min((int64_t)C, te - t0);
       const uint32_t stride = (uint32_t)p.x_heads * (D * ES);
@@ -854,6 +863,9 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   load_x(0);
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
+  // A state that only bf16 outputs are taken from needs no third term of the
+  // weighted values: two cut at 16 bits are far below the outputs' rounding.
+  const bool fp32_state = DG || !OUT || (p.fin && (REV ? first : last));
   uint32_t base = lds0;  // of the chunk's query and key tiles
   read_q(base, 0);
   read_q(base, 1);
@@ -862,24 +874,12 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     const int nv = (int)min((int64_t)C, te - t0);
     const int b = ci & 3;
 
-    // what the decays' gradient needs of the states at boundaries
-    if constexpr (DG && !REV) {
-      if (p.fwd_snap != p.snap && (t0 - bos) % p.anchor == 0) store_state(anchor_state((t0 - bos) / p.anchor), accS);
-    }
+    if constexpr (DG && !REV)
+      if (p.anchors != p.snap && (t0 - bos) % p.anchor == 0) leave_state((t0 - bos) / p.anchor, accS);
     if constexpr (DK) {
       const int64_t tend = t0 + nv;
-      if (tend == te || (tend - bos) % p.anchor == 0) {
-        f32x4 x[8];
-        load_state(anchor_state((tend - bos + p.anchor - 1) / p.anchor), x);
-        float dot = 0.f;
-#pragma unroll
-        for (int rt = 0; rt < 8; ++rt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dot += x[rt][i] * accS[rt][i];
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m);
-        if (lane == 0) sAnc[b * NW + wv] = dot;
-      }
+      if (p.anchors != p.snap && (tend == te || (tend - bos) % p.anchor == 0))
+        leave_state((tend - bos + p.anchor - 1) / p.anchor - 1, accS);
     }
     chunk_barrier();
 
@@ -887,20 +887,23 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     // use (at most 15 can be waited for one by one); the vector arithmetic
     // fills the gaps between products.
     const uint32_t base_next = base + L::SET == lds0 + NBUF * L::SET ? lds0 : base + L::SET;
-    const uint32_t vbase = DK ? base + L::V : lds0 + L::VALS + (ci & 1) * L::VTILE;
+    const uint32_t vbase = lds0 + L::VALS + (ci & 1) * L::VTILE;
     const float gam = sGam[b];
     float w[KT][TN];
     TF fv[KT], fk[8];
+    auto read_values = [&]() {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
+      for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int i = 0; i < TN; i += 4) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + 4 * TN * kt + TN * g + i);
+        for (int i = 0; i < TN; i += 4) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + 4 * TN * kt + TN * g + i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
+          for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
+        }
+        ld_col(fv[kt], vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
       }
-      ld_col(fv[kt], vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
-    }
+    };
+    if constexpr (!DG) read_values();
     auto read_k = [&](int kt, int first, int count) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt)
@@ -916,9 +919,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
     };
     auto add_to_state = [&](int kt) {
 #pragma unroll
-      for (int s = 0; s < NSV; ++s)
+      for (int s = 0; s < NSV; ++s) {
+        if (OUT && !DG && s == 2 && !fp32_state) break;
 #pragma unroll
         for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][s]);
+      }
     };
     f32x4 accO[OUT ? NT : 1];
     if constexpr (OUT) {
@@ -928,23 +933,39 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
       for (int rt = 0; rt < NT; ++rt) row[rt] = sRow[b * C + 16 * rt + l16];
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) accO[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        Frag<E> fs[NSS];
+      Frag<E> fs[2][NSS];
+      auto split_state = [&](int ks) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[i] = accS[2 * ks][i];
           x[4 + i] = accS[2 * ks + 1][i];
         }
-        split<NSS>(fs, x);
+        split<NSS>(fs[ks & 1], x);
+      };
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        if (ks == 0) split_state(0);
+        if (ks < 3) split_state(ks + 1);
 #pragma unroll
         for (int s = 0; s < NSS; ++s)
 #pragma unroll
-          for (int rt = 0; rt < NT; ++rt) accO[rt] = mma(accO[rt], fs[s], fq[ks & 1][rt]);
+          for (int rt = 0; rt < NT; ++rt) accO[rt] = mma(accO[rt], fs[ks & 1][s], fq[ks & 1][rt]);
+        if constexpr (NSS > 1) {
+          // the next step's operands are cut between this one's products
+#pragma unroll
+          for (int i = 0; i < NSS * NT; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+          }
+        }
         if (ks < 2) read_q(base, ks + 2);
-        else read_k(0, 2 * (ks - 2), 2);
+        else if (!DG) read_k(0, 2 * (ks - 2), 2);
         __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (DG) {  // (no registers for them earlier)
+        read_values();
+        read_k(0, 0, 4);
       }
       weigh_values(0);
       TF fp[NT][KT];
@@ -954,27 +975,29 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
         for (int kt = 0; kt < KT; ++kt)
           if (REV ? kt >= rt / TPS : kt <= rt / TPS)
             ld_pair(fp[rt][kt], lds0 + L::PAIR + (ci & 1) * (C * L::RB) + p_at[kt] + 16 * rt * L::RB);
-      read_k(0, 4, 4);
+      if constexpr (!DG) read_k(0, 4, 4);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int rt = 0; rt < NT; ++rt) {
-        accO[rt] *= row[rt];
-        if constexpr (DG) {
-          float dot = 0.f;
-          Frag16<E> fx;
-          if constexpr (REV)
-            ld_frag16(fx, reinterpret_cast<const E*>(smem + (base - lds0) + L::X + tile_at<E, D>(l16, col0 + 4 * g) + 16 * rt * (D * ES)));
-          else
-            fx.v = __builtin_bit_cast(decltype(fx.v), xr[rt]);
-          const f32x4 x = frag16_to_f32(fx);
+      for (int rt = 0; rt < NT; ++rt) accO[rt] *= row[rt];
+      if constexpr (DG) {
+        float dot[NT];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dot += x[i] * accO[rt][i];
-          dot += __shfl_xor(dot, 16);
-          dot += __shfl_xor(dot, 32);
-          if (g == 0) sRX[((ci & 1) * NW + wv) * C + 16 * rt + l16] = dot;
+        for (int rt = 0; rt < NT; ++rt) {
+          Frag16<E> fx;
+          fx.v = __builtin_bit_cast(decltype(fx.v), xr[rt]);
+          const f32x4 x = frag16_to_f32(fx);
+          dot[rt] = x[0] * accO[rt][0];
+#pragma unroll
+          for (int i = 1; i < 4; ++i) dot[rt] += x[i] * accO[rt][i];
         }
+        int tile;
+        const float sum = sum_groups(dot, g, tile);
+        if (tile >= 0) sRX[((ci & 1) * NW + wv) * C + 16 * tile + l16] = sum;
       }
-      load_x(ci + 1);
+      if constexpr (DG) {
+        load_x(ci + 1);
+        read_k(0, 4, 4);
+      }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -1023,46 +1046,177 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   if (OUT) {
     if (p.fin && (REV ? first : last)) store_state(p.fin + nh * kState, accS);
     if constexpr (DG && !REV)
-      if (last && nch > 0) store_state(anchor_state((eos - bos + p.anchor - 1) / p.anchor), accS);
+      if (last && nch > 0) leave_state((eos - bos + p.anchor - 1) / p.anchor, accS);
   } else {
     store_state(p.snap + ((size_t)slot * H + h) * kState, accS);
   }
 }
 
-template <typename E, int NW, bool REV, bool TR, bool OUT, bool DG>
-hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
-  using L = WalkLayout<E, NW, DG, DG && REV>;
+// Blocks b and b + 8 run on the same XCD: what the blocks of one work item
+// (PER of them) both read comes from its L2 the second time.
+template <int PER>
+__device__ __forceinline__ int64_t work_item(int& part) {
+  const int64_t slot8 = blockIdx.x >> 3;
+  part = (int)(slot8 % PER);
+  return (slot8 / PER) * 8 + (blockIdx.x & 7);
+}
+
+template <typename E, int NW, bool REV, bool OUT>
+__global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  int cb;
+  const int64_t u = work_item<8 / NW>(cb);
+  if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, cb);
+}
+
+// The three gradients' walks of every work item, side by side.  The walks that
+// go backwards read the same tensors at about the same time.
+template <typename E, int NW, bool DG>
+__global__ __launch_bounds__(64 * (NW + 4)) void linear_grad_kernel(const LinearGradArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int CB = 8 / NW;
-  const int64_t blocks = (a.units + 7) / 8 * 8 * CB;
-  static std::atomic<bool> set[64];
+  int part;
+  const int64_t u = work_item<3 * CB>(part);
+  if (u >= p.dq.units) return;
+  const int cb = part % CB;
+  if (part < CB) walk<E, NW, true, true, true, DG>(p.dk, smem, u, cb);
+  else if (part < 2 * CB) walk<E, NW, true, false, true, false>(p.dv, smem, u, cb);
+  else walk<E, NW, false, true, true, DG>(p.dq, smem, u, cb);
+}
+
+// Dynamic LDS above 64 KiB has to be asked for, once per device.
+template <typename K>
+hipError_t allow_lds(K kernel, int bytes, std::atomic<bool> (&set)[64]) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  if (dev < 0 || dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(linear_walk_kernel<E, NW, REV, TR, OUT, DG>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-    if (e != hipSuccess) return e;
-    if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_relaxed);
-  }
-  hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, TR, OUT, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), L::BYTES, stream, a);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && set[dev].load(std::memory_order_relaxed)) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess && known) set[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename E, int NW, bool REV, bool OUT>
+hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
+  constexpr int LDS = WalkLayout<E, NW, false, false>::BYTES;
+  static std::atomic<bool> set[64];
+  hipError_t e = allow_lds(linear_walk_kernel<E, NW, REV, OUT>, LDS, set);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (a.units + 7) / 8 * 8 * (8 / NW);
+  hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, OUT>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
   return hipGetLastError();
 }
 
 template <typename E>
 hipError_t launch_walk_e(const LinearWalkArgs& a, hipStream_t stream) {
-  if (!a.write_o)
-    return a.reverse ? launch_walk_t<E, 8, true, false, false, false>(a, stream)
-                     : launch_walk_t<E, 8, false, false, false, false>(a, stream);
-  if (a.transposed) {
-    if (a.reverse)
-      return a.with_decay_grad ? launch_walk_t<E, 8, true, true, true, true>(a, stream)
-                               : launch_walk_t<E, 8, true, true, true, false>(a, stream);
-    return a.with_decay_grad ? launch_walk_t<E, 8, false, true, true, true>(a, stream)
-                             : launch_walk_t<E, 8, false, true, true, false>(a, stream);
+  if (!a.write_o) return a.reverse ? launch_walk_t<E, 8, true, false>(a, stream) : launch_walk_t<E, 8, false, false>(a, stream);
+  return a.narrow ? launch_walk_t<E, 4, false, true>(a, stream) : launch_walk_t<E, 8, false, true>(a, stream);
+}
+
+template <typename E, int NW, bool DG>
+hipError_t launch_grad_t(const LinearGradArgs& a, hipStream_t stream) {
+  constexpr int LDS = std::max({WalkLayout<E, NW, DG, DG>::BYTES, WalkLayout<E, NW, DG, false>::BYTES,
+                                WalkLayout<E, NW, false, false>::BYTES});
+  static std::atomic<bool> set[64];
+  hipError_t e = allow_lds(linear_grad_kernel<E, NW, DG>, LDS, set);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (a.dq.units + 7) / 8 * 8 * 3 * (8 / NW);
+  hipLaunchKernelGGL((linear_grad_kernel<E, NW, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_grad_e(const LinearGradArgs& a, hipStream_t stream) {
+  if (a.dq.narrow) return a.decay_grad ? launch_grad_t<E, 4, true>(a, stream) : launch_grad_t<E, 4, false>(a, stream);
+  return a.decay_grad ? launch_grad_t<E, 8, true>(a, stream) : launch_grad_t<E, 8, false>(a, stream);
+}
+
+// ---------------------------------------------------------------------------
+// The decays' gradient of one (stretch of `anchor` tokens, head):
+//   D_t = <S, dS> at the stretch's end + sum over t' >= t of r_t' - c_t',
+// in fp64, from the stretch's end on, 1024 tokens a turn (four a thread).
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void linear_decay_grad_kernel(const LinearDecayGradArgs a) {
+  constexpr size_t kState = (size_t)D * D;
+  const int H = a.num_heads;
+  const int h = (int)(blockIdx.x % H);
+  const int64_t slot = blockIdx.x / H;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  __shared__ double part[4];
+  auto block_sum = [&](double x) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m);
+    if (lane == 0) part[wv] = x;
+    __syncthreads();
+    const double y = ((part[0] + part[1]) + part[2]) + part[3];
+    __syncthreads();
+    return y;
+  };
+  const Segment s = find_segment(a.cu, a.num_seqs, a.total_tokens, a.anchor, slot);
+  double total = 0.0;
+  if (s.ok && s.count > 0) {
+    const int64_t tb = s.bos + (int64_t)s.j * a.anchor, te = min(s.eos, tb + (int64_t)a.anchor);
+    double flow = 0.0;
+    if (s.j + 1 < s.count || a.has_d_final) {
+      const float* S = a.s_anchors + ((size_t)(slot + 1) * H + h) * kState;  // entering the next stretch
+      const float* M = a.ds_anchors + ((size_t)slot * H + h) * kState;
+      double d = 0.0;
+      for (int i = 0; i < 16; ++i) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(S + i * 1024 + 4 * t);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(M + i * 1024 + 4 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d += (double)x[j] * (double)y[j];
+      }
+      flow = block_sum(d);
+    }
+    const size_t half = (size_t)H * a.total_tokens;
+    for (int64_t b = tb + (te - 1 - tb) / 1024 * 1024; b >= tb; b -= 1024) {
+      double x[4];
+      double mine = 0.0;
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        const int64_t at = b + 4 * t + j;
+        double c = 0.0;
+        if (at < te) {
+          const size_t i = (size_t)h * a.total_tokens + at;
+          for (int k = 0; k < a.blocks; ++k) c += (double)a.r[k * half + i] - (double)a.c[k * half + i];
+        }
+        mine += c;
+        x[j] = mine;  // from token at to the last of this thread's
+      }
+      // what the threads behind this one sum to
+      double w = mine;
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const double o = __shfl_down(w, m);
+        if (lane + m < 64) w += o;
+      }
+      if (lane == 0) part[wv] = w;
+      __syncthreads();
+      double behind = w - mine, all = 0.0;
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        if (k > wv) behind += part[k];
+        all += part[k];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = b + 4 * t + j;
+        if (at < te) {
+          const double d = flow + behind + x[j];
+          if (a.d_log_decay) a.d_log_decay[(size_t)at * H + h] = (float)d;
+          total += d;
+        }
+      }
+      flow += all;
+    }
   }
-  if (a.reverse) return launch_walk_t<E, 8, true, false, true, false>(a, stream);
-  return a.narrow ? launch_walk_t<E, 4, false, false, true, false>(a, stream)
-                  : launch_walk_t<E, 8, false, false, true, false>(a, stream);
+  if (a.part) {
+    const double y = block_sum(total);
+    if (t == 0) a.part[blockIdx.x] = y;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1109,7 +1263,9 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a
 // ---------------------------------------------------------------------------
 template <typename E>
 __global__ __launch_bounds__(256) void linear_share_sum_kernel(const float* __restrict__ src, E* __restrict__ dst,
-                                                               int64_t rows, int share) {
+                                                               const int32_t* cu, int num_seqs, int64_t total_tokens,
+                                                               int heads, int share) {
+  const int64_t rows = (cu ? clamp_cu(cu, num_seqs, total_tokens) : total_tokens) * heads;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = i >> 5;
   const int ch = (int)(i & 31) * 4;
@@ -1135,6 +1291,16 @@ hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream) {
   return a.bf16 ? launch_walk_e<__bf16>(a, stream) : launch_walk_e<float>(a, stream);
 }
 
+hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream) {
+  return a.dq.bf16 ? launch_grad_e<__bf16>(a, stream) : launch_grad_e<float>(a, stream);
+}
+
+hipError_t launch_linear_decay_grad(const LinearDecayGradArgs& a, hipStream_t stream) {
+  const int64_t blocks = linear_slots(a.total_tokens, a.num_seqs, a.anchor) * a.num_heads;
+  hipLaunchKernelGGL(linear_decay_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream) {
   const int64_t blocks = (int64_t)a.num_seqs * a.num_heads * 16;
   if (a.reverse)
@@ -1144,16 +1310,16 @@ hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_share_sum(const float* src, void* dst, int64_t rows, int share, bool bf16,
-                                   hipStream_t stream) {
-  const int64_t blocks = (rows * 32 + 255) / 256;
+hipError_t launch_linear_share_sum(const float* src, void* dst, const LinearWalkArgs& a, hipStream_t stream) {
+  const int heads = a.x_heads, share = a.num_heads / heads;
+  const int64_t blocks = (a.total_tokens * heads * 32 + 255) / 256;
   if (blocks == 0) return hipSuccess;
-  if (bf16)
+  if (a.bf16)
     hipLaunchKernelGGL(linear_share_sum_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, stream, src,
-                       static_cast<__bf16*>(dst), rows, share);
+                       static_cast<__bf16*>(dst), a.cu, a.num_seqs, a.total_tokens, heads, share);
   else
     hipLaunchKernelGGL(linear_share_sum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, stream, src,
-                       static_cast<float*>(dst), rows, share);
+                       static_cast<float*>(dst), a.cu, a.num_seqs, a.total_tokens, heads, share);
   return hipGetLastError();
 }
 

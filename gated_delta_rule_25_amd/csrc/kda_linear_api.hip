@@ -37,10 +37,12 @@ struct LinearPlan {
   bool segmented = false;
   bool narrow = false;
   int64_t seg = kAnchorTokens;
-  int64_t slots = 0;  // segments, empty ones included
+  int64_t slots = 0;     // segments, empty ones included
+  int64_t anchored = 0;  // stretches of the decays' gradient, likewise
   int64_t anchor = kAnchorTokens;
-  bool own_snaps = false;  // boundary states apart from the segments'
-  size_t off_fsnap = 0, off_rsnap = 0, off_anchor = 0, off_decay = 0, off_row = 0, off_part = 0, off_share = 0;
+  bool own_anchors = false;  // boundary states apart from the segments'
+  int blocks = 1;            // column blocks of a head
+  size_t off_fsnap = 0, off_rsnap = 0, off_anchor = 0, off_decay = 0, off_change = 0, off_part = 0, off_share = 0;
   size_t bytes = 0;
 };
 
@@ -58,11 +60,11 @@ struct LinearPlan {
 void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
                      bool backward) {
   const int64_t units = (int64_t)num_seqs * num_heads;
-  pl.narrow = !backward && units < cus;
+  pl.narrow = units < cus;
   if (segment_tokens > 0) {
     pl.segmented = true;
     pl.seg = segment_tokens;
-  } else if (segment_tokens == 0 && (backward ? units : 3 * units) < cus) {
+  } else if (segment_tokens == 0 && (backward ? 6 : 3) * units < cus) {
     const int64_t target = (int64_t)cus * (backward ? 3 : 1);
     int64_t seg = (total_tokens * num_heads + target - 1) / target;
     seg = std::max((seg + 255) / 256 * 256, kMinSegment);
@@ -76,7 +78,7 @@ void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num
 }
 
 bool plan_ok(const LinearPlan& pl, int num_heads) {
-  return pl.slots * num_heads <= (int64_t)INT32_MAX / 4;
+  return std::max(pl.slots, pl.anchored) * num_heads <= (int64_t)INT32_MAX / 4;
 }
 
 LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus) {
@@ -95,10 +97,10 @@ LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
 }
 
 // Pieces, each 256-byte aligned: segmented, S and dS at the segment
-// boundaries ([slots][H] states); S at the boundaries of the decays' gradient
-// where those are others; the segments' decays [slots][H]; r_t's part through
-// the state [T, H]; the per-item sums of a constant decay's gradient; the fp32
-// gradient [T, H, 128] that shared heads are summed from.
+// boundaries ([slots][H] states); both at the boundaries of the decays'
+// gradient where those are others; the segments' decays [slots][H]; r_t and
+// c_t [column blocks][H][T]; the stretches' sums of a constant decay's
+// gradient; the fp32 gradients [T, H, 128] that shared heads are summed from.
 LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads, int segment_tokens,
                          bool decay_grad, bool decay_per_head, int cus) {
   LinearPlan pl;
@@ -113,23 +115,25 @@ LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
     while (pl.seg % (64 * parts) != 0) ++parts;  // ends at seg / 64
     pl.anchor = pl.seg / parts;
   }
-  pl.own_snaps = decay_grad && !(pl.segmented && pl.anchor == pl.seg);
+  pl.own_anchors = decay_grad && !(pl.segmented && pl.anchor == pl.seg);
+  pl.anchored = decay_grad ? kda::linear_slots(total_tokens, num_seqs, pl.anchor) : 0;
+  const size_t anchored = (size_t)pl.anchored * num_heads;
+  pl.blocks = pl.narrow ? 2 : 1;
   size_t off = 0;
   pl.off_fsnap = off;
   if (pl.segmented) off += units * kStateBytes;
   pl.off_rsnap = off;
   if (pl.segmented) off += units * kStateBytes;
   pl.off_anchor = off;
-  if (pl.own_snaps) off += (size_t)kda::linear_slots(total_tokens, num_seqs, pl.anchor) * num_heads * kStateBytes;
+  if (pl.own_anchors) off += 2 * anchored * kStateBytes;
   pl.off_decay = off;
   if (pl.segmented) off += align256(units * sizeof(float));
-  pl.off_row = off;
-  if (decay_grad) off += align256(rows * sizeof(float));
+  pl.off_change = off;
+  if (decay_grad) off += align256(2 * pl.blocks * rows * sizeof(float));
   pl.off_part = off;
-  if (decay_grad && decay_per_head)
-    off += align256((pl.segmented ? units : (size_t)num_seqs * num_heads) * sizeof(double));
+  if (decay_grad && decay_per_head) off += align256(anchored * sizeof(double));
   pl.off_share = off;
-  if (num_qk_heads != num_heads) off += rows * kD * sizeof(float);
+  if (num_qk_heads != num_heads) off += 2 * rows * kD * sizeof(float);
   pl.bytes = off;
   return pl;
 }
@@ -164,9 +168,7 @@ bool any_overlap(const Range* outs, size_t no, const Range* ins, size_t ni) {
 // Incoming states of the segments: their own contributions, then the scan.
 hipError_t segment_states(kda::LinearWalkArgs w, const float* init, hipStream_t stream) {
   w.write_o = false;
-  w.transposed = false;
   w.narrow = false;
-  w.with_decay_grad = false;
   hipError_t e = kda::launch_linear_walk(w, stream);
   if (e != hipSuccess) return e;
   kda::LinearScanArgs s;
@@ -329,12 +331,15 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
 
   char* ws = static_cast<char*>(workspace);
   const bool shared = num_qk_heads != num_heads;
-  float* share = shared ? reinterpret_cast<float*>(ws + pl.off_share) : nullptr;
-  float* fsnap = reinterpret_cast<float*>(ws + pl.off_fsnap);
-  float* rsnap = reinterpret_cast<float*>(ws + pl.off_rsnap);
-  float* seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
-  float* anchors = pl.own_snaps ? reinterpret_cast<float*>(ws + pl.off_anchor) : fsnap;
-  double* part = grad && per_head ? reinterpret_cast<double*>(ws + pl.off_part) : nullptr;
+  const size_t rows = (size_t)total_tokens * num_heads;
+  float* share = reinterpret_cast<float*>(ws + pl.off_share);  // of dq, then of dk
+  float* fsnap = pl.segmented ? reinterpret_cast<float*>(ws + pl.off_fsnap) : nullptr;
+  float* rsnap = pl.segmented ? reinterpret_cast<float*>(ws + pl.off_rsnap) : nullptr;
+  const size_t anchored = (size_t)pl.anchored * num_heads;
+  float* anchors = reinterpret_cast<float*>(ws + pl.off_anchor);
+  float* s_anchors = pl.own_anchors ? anchors : fsnap;
+  float* ds_anchors = pl.own_anchors ? anchors + anchored * kD * kD : rsnap;
+  float* change = reinterpret_cast<float*>(ws + pl.off_change);
 
   kda::LinearWalkArgs base;
   std::memset(&base, 0, sizeof(base));
@@ -348,73 +353,81 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   base.seg = (int)pl.seg;
   base.anchor = (int)pl.anchor;
   base.segmented = pl.segmented;
+  base.narrow = pl.narrow;
   base.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
-  base.seg_decay = seg_decay;
+  base.seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
   base.write_o = true;
-  auto role = [&](kda::LinearWalkArgs& w, const void* a, int ah, const void* b, int bh, const void* c, int ch) {
+  const int hq = num_qk_heads, hv = num_heads;
+  auto role = [](kda::LinearWalkArgs w, const void* a, int ah, const void* b, int bh, const void* c, int ch) {
     w.q = a;
     w.q_heads = ah;
     w.k = b;
     w.k_heads = bh;
     w.v = c;
     w.v_heads = ch;
+    w.x_heads = ch;
+    return w;
   };
-  const int hq = num_qk_heads, hv = num_heads;
-
-  // dq: forwards with S^T
-  kda::LinearWalkArgs w = base;
+  kda::LinearGradArgs g;
+  g.decay_grad = grad;
+  g.dq = role(base, d_o, hv, v, hv, k, hq);
+  g.dq.init = initial_state;
+  g.dq.snap = fsnap;
+  g.dq.x = q;
+  g.dq.x_heads = hq;
+  g.dq.anchors = s_anchors;
+  g.dq.change = change;
+  g.dq.o = shared ? static_cast<void*>(share) : dq;
+  g.dq.o_f32 = shared;
+  base.reverse = true;
+  base.init = d_final_state;
+  base.snap = rsnap;
+  g.dk = role(base, v, hv, d_o, hv, q, hq);
+  g.dk.x = k;
+  g.dk.x_heads = hq;
+  g.dk.anchors = ds_anchors;
+  g.dk.change = change + pl.blocks * rows;
+  g.dk.o = shared ? static_cast<void*>(share + rows * kD) : dk;
+  g.dk.o_f32 = shared;
+  g.dv = role(base, k, hq, q, hq, d_o, hv);
+  g.dv.fin = d_initial_state;
+  g.dv.o = dv;
   if (pl.segmented) {
-    role(w, nullptr, hq, k, hq, v, hv);
-    w.snap = fsnap;
-    if (segment_states(w, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
+    kda::LinearWalkArgs f = role(g.dq, nullptr, hq, k, hq, v, hv);
+    if (segment_states(f, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
+    if (segment_states(g.dv, d_final_state, stream) != hipSuccess) return KDA_ERR_HIP;
   }
-  role(w, d_o, hv, v, hv, k, hq);
-  w.transposed = true;
-  w.with_decay_grad = grad;
-  w.x = q;
-  w.x_heads = hq;
-  w.init = initial_state;
-  w.fwd_snap = anchors;
-  w.row_dot = reinterpret_cast<float*>(ws + pl.off_row);
-  w.o = shared ? static_cast<void*>(share) : dq;
-  w.o_f32 = shared;
-  if (kda::launch_linear_walk(w, stream) != hipSuccess) return KDA_ERR_HIP;
-  const int64_t qk_rows = total_tokens * num_qk_heads;
-  if (shared && kda::launch_linear_share_sum(share, dq, qk_rows, hv / hq, base.bf16, stream) != hipSuccess)
-    return KDA_ERR_HIP;
-
-  // dk: backwards with dS^T; it also forms the decays' gradient
-  kda::LinearWalkArgs r = base;
-  r.reverse = true;
-  r.init = d_final_state;
-  if (pl.segmented) {
-    role(r, nullptr, hq, q, hq, d_o, hv);
-    r.snap = rsnap;
-    if (segment_states(r, d_final_state, stream) != hipSuccess) return KDA_ERR_HIP;
+  if (kda::launch_linear_grad(g, stream) != hipSuccess) return KDA_ERR_HIP;
+  if (grad && total_tokens > 0) {
+    kda::LinearDecayGradArgs d;
+    std::memset(&d, 0, sizeof(d));
+    d.s_anchors = s_anchors;
+    d.ds_anchors = ds_anchors;
+    d.r = change;
+    d.c = change + pl.blocks * rows;
+    d.blocks = pl.blocks;
+    d.has_d_final = d_final_state != nullptr;
+    d.d_log_decay = per_head ? nullptr : d_log_decay;
+    d.part = per_head ? reinterpret_cast<double*>(ws + pl.off_part) : nullptr;
+    d.cu = cu_seqlens;
+    d.num_seqs = num_seqs;
+    d.total_tokens = total_tokens;
+    d.num_heads = num_heads;
+    d.anchor = (int)pl.anchor;
+    if (kda::launch_linear_decay_grad(d, stream) != hipSuccess) return KDA_ERR_HIP;
   }
-  kda::LinearWalkArgs x = r;
-  role(x, v, hv, d_o, hv, q, hq);
-  x.transposed = true;
-  x.with_decay_grad = grad;
-  x.x = k;
-  x.x_heads = hq;
-  x.fwd_snap = anchors;
-  x.row_dot = w.row_dot;
-  x.d_log_decay = per_head ? nullptr : d_log_decay;
-  x.d_decay_part = part;
-  x.o = shared ? static_cast<void*>(share) : dk;
-  x.o_f32 = shared;
-  if (kda::launch_linear_walk(x, stream) != hipSuccess) return KDA_ERR_HIP;
-  if (shared && kda::launch_linear_share_sum(share, dk, qk_rows, hv / hq, base.bf16, stream) != hipSuccess)
-    return KDA_ERR_HIP;
-  if (part && kda::launch_linear_decay_sum(part, d_log_decay, base.units, num_heads, stream) != hipSuccess)
-    return KDA_ERR_HIP;
-
-  // dv: backwards with dS
-  role(r, k, hq, q, hq, d_o, hv);
-  r.fin = d_initial_state;
-  r.o = dv;
-  return kda::launch_linear_walk(r, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+  if (grad && per_head) {
+    // (no tokens: no stretch, and the sums are zero)
+    const int64_t units = total_tokens > 0 ? (int64_t)anchored : 0;
+    if (kda::launch_linear_decay_sum(reinterpret_cast<double*>(ws + pl.off_part), d_log_decay, units, num_heads,
+                                     stream) != hipSuccess)
+      return KDA_ERR_HIP;
+  }
+  if (shared) {
+    if (kda::launch_linear_share_sum(share, dq, g.dq, stream) != hipSuccess) return KDA_ERR_HIP;
+    if (kda::launch_linear_share_sum(share + rows * kD, dk, g.dk, stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  return KDA_OK;
 }
 
 kda_status kda_linear_decode_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,

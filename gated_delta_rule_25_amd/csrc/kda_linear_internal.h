@@ -42,10 +42,8 @@ struct LinearWalkArgs {
   bool segmented;          // work items are (segment, head), else (sequence, head)
   int64_t units;           // work items
   bool reverse;            // backwards in time
-  bool transposed;         // the walked state is the transpose of what is stored
   bool write_o;            // false: only each segment's own contribution to the state
   bool narrow;             // 64 value columns per workgroup instead of 128
-  bool with_decay_grad;
   const float* init;       // [N,H,128,128] or null (zero): enters at the sequence's first (reverse: last) token
   float* fin;              // [N,H,128,128] or null: the state behind the last (reverse: before the first) token
   float* snap;             // [slots][H][128,128] segmented: incoming states; states pass: contributions (written)
@@ -54,11 +52,32 @@ struct LinearWalkArgs {
   bool o_f32;
   // gradient of the decays
   int anchor;              // tokens between the boundaries at which it is taken from the states (a multiple of 64)
-  float* fwd_snap;         // [slots by `anchor`][H][128,128]: S at every boundary, and behind the last token
-                           // (`snap` itself when segments are of that length)
-  float* row_dot;          // [T, H]: q_t . dq_t's part through the state (dq walk writes, dk walk reads)
-  float* d_log_decay;      // [T, H] or null (dk walk)
-  double* d_decay_part;    // decay_per_head: [work items] sums (dk walk), else null
+  float* anchors;          // [slots by `anchor`][H][128,128]: dq walk: S entering every stretch, and behind the last
+                           // token; dk walk: dS behind every stretch (written; `snap` itself when segments are of
+                           // that length and the scan has left them there)
+  float* change;           // [column blocks][H][T]: r_t (dq walk) or c_t (dk walk) by the block's columns (written)
+};
+
+// The three walks of the backward pass.
+struct LinearGradArgs {
+  LinearWalkArgs dq, dk, dv;
+  bool decay_grad;
+};
+
+struct LinearDecayGradArgs {
+  const float* s_anchors;
+  const float* ds_anchors;
+  const float* r;          // [blocks][H][T]
+  const float* c;
+  int blocks;
+  bool has_d_final;        // dS behind a sequence's last token is not zero
+  float* d_log_decay;      // [T, H] or null
+  double* part;            // [slots by `anchor`][H] sums over the stretch (a constant decay), or null
+  const int32_t* cu;
+  int num_seqs;
+  int64_t total_tokens;
+  int num_heads;
+  int anchor;
 };
 
 struct LinearScanArgs {
@@ -88,10 +107,11 @@ struct LinearDecodeArgs {
 };
 
 hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream);
+hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream);
+hipError_t launch_linear_decay_grad(const LinearDecayGradArgs& a, hipStream_t stream);
 hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream);
 // dst[t][g] = sum over the `share` heads of group g of src[t][g share + i], fp32 to the I/O dtype.
-hipError_t launch_linear_share_sum(const float* src, void* dst, int64_t rows, int share, bool bf16,
-                                   hipStream_t stream);
+hipError_t launch_linear_share_sum(const float* src, void* dst, const LinearWalkArgs& a, hipStream_t stream);
 // dst[h] = sum over the work items u with u % num_heads = h of part[u], in order.
 hipError_t launch_linear_decay_sum(const double* part, float* dst, int64_t units, int num_heads, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearDecodeArgs& a, hipStream_t stream);
