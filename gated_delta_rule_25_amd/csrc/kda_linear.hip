@@ -486,12 +486,11 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   const int nch = (int)((te - tb + C - 1) / C);
   const size_t nh = (size_t)n * H + h;
   auto chunk_of = [&](int ci) { return REV ? nch - 1 - ci : ci; };
-  // whether the state behind chunk ci (in the walk's order) is at a boundary
-  // where the decays' gradient takes it from memory or leaves it there
-  auto at_anchor = [&](int ci) {
-    const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
-    return ((REV ? t0 : t0 + C) - bos) % p.anchor == 0;
-  };
+  // Boundaries where the decays' gradient takes the state from memory or leaves
+  // it there (an item begins at one): chunks from one to the next, and from the
+  // walk's start to the first behind it.
+  const int stretch = DG ? p.anchor / C : 0;
+  const int stretch0 = DG && REV ? (nch + stretch - 1) % stretch + 1 : stretch;
   // Iteration ci (from -1): compute waves on chunk ci, pair waves on ci + 1,
   // decay wave on ci + 2 and back on ci - 1.
 
@@ -567,6 +566,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     };
     double log_total = 0.0;
     double scale = 0.0;  // s: the state is 2^s times the accumulators
+    int boundary = stretch0;
     auto put_decay = [&](int ci, float la) {
       const int64_t t = tb + (int64_t)chunk_of(ci) * C + lane;
       const double s = prefix_sum<C>((double)fmaxf(la, kMinLogDecay) * kLog2e, lane);
@@ -575,7 +575,9 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       const double before = scale;
       scale += tot;
       float gam = 1.f;
-      if (scale < kScaleFloor || ci == nch - 1 || (DG && at_anchor(ci))) {
+      const bool at_boundary = DG && --boundary == 0;  // the state behind the chunk is wanted
+      if (at_boundary) boundary = stretch;
+      if (scale < kScaleFloor || ci == nch - 1 || at_boundary) {
         gam = exp2_fast((float)scale);
         scale = 0.0;
       }
@@ -869,17 +871,20 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   uint32_t base = lds0;  // of the chunk's query and key tiles
   read_q(base, 0);
   read_q(base, 1);
+  int boundary = 0;  // chunks to the next one
+  int64_t stretch_at = DG ? (REV ? (te - bos + p.anchor - 1) / p.anchor - 1 : (tb - bos) / p.anchor) : 0;
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
     const int b = ci & 3;
 
-    if constexpr (DG && !REV)
-      if (p.anchors != p.snap && (t0 - bos) % p.anchor == 0) leave_state((t0 - bos) / p.anchor, accS);
-    if constexpr (DK) {
-      const int64_t tend = t0 + nv;
-      if (p.anchors != p.snap && (tend == te || (tend - bos) % p.anchor == 0))
-        leave_state((tend - bos + p.anchor - 1) / p.anchor - 1, accS);
+    if constexpr (DG) {
+      if (boundary == 0) {
+        if (p.anchors != p.snap) leave_state(stretch_at, accS);
+        stretch_at += REV ? -1 : 1;
+        boundary = ci == 0 ? stretch0 : stretch;
+      }
+      --boundary;
     }
     chunk_barrier();
 
