@@ -247,14 +247,14 @@ __device__ __forceinline__ float frag_get(const Frag<__bf16>& f, int i) { return
 __device__ __forceinline__ float frag_get(const Frag16<float>& f, int i) { return f.v[i]; }
 
 // x as the sum of NS operands.  bf16, one term: rounded to nearest.  Three
-// terms: the 24 significant bits cut in three (each subtraction is exact), the
-// high halves of two words packed by one byte permutation.  fp32: itself.
+// terms: the 24 significant bits cut in three (each subtraction is exact; two
+// terms: the first 16), the high halves of two words packed by one byte permutation.  fp32: itself.
 template <int NS>
 __device__ __forceinline__ void split(Frag<__bf16> (&f)[NS], const float (&x)[8]) {
   if constexpr (NS == 1) {
     frag_from_f32(f[0], x);
   } else {
-    static_assert(NS == 3, "one or three terms");
+    static_assert(NS == 2 || NS == 3, "one to three terms");
     uint32_t t[3][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -264,7 +264,7 @@ __device__ __forceinline__ void split(Frag<__bf16> (&f)[NS], const float (&x)[8]
       t[2][i] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, t[1][i] & 0xffff0000u));
     }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < NS; ++s) {
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(t[s][2 * i + 1], t[s][2 * i], 0x07060302u);
@@ -439,7 +439,8 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   constexpr int TN = Tok<E>::N;
   constexpr int C = L::C, NT = C / 16, ES = L::ES, NBUF = L::NBUF;
   constexpr bool BF = ES == 2;
-  constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values
+  constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values,
+  constexpr int MSV = OUT && !DG ? std::min(NSV, 2) : NSV;  // of which are always taken
   constexpr int NSS = (BF && DG) ? 3 : 1;      // terms of the state in the outputs' product
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
   constexpr int KT = C / (4 * TN);             // token steps per chunk
@@ -925,10 +926,16 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     auto add_to_state = [&](int kt) {
 #pragma unroll
       for (int s = 0; s < NSV; ++s) {
-        if (OUT && !DG && s == 2 && !fp32_state) break;
+        if (s >= MSV) continue;
 #pragma unroll
         for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][s]);
       }
+    };
+    auto add_rest = [&](int kt) {
+      if constexpr (MSV < NSV)
+        if (fp32_state)
+#pragma unroll
+          for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][NSV - 1]);
     };
     f32x4 accO[OUT ? NT : 1];
     if constexpr (OUT) {
@@ -1017,13 +1024,25 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt) accS[rt] *= gam;
     }
-    // state, with the outputs' stores in between
+    // State.  The first step's products cover the second one's weighted values
+    // and, as its keys come free, their reads; the second step's cover the
+    // outputs' stores and the reads of the next chunk's queries (its tiles are
+    // in LDS already; the last chunk reads what is there and drops it).
+    static_assert(KT == 2, "two token steps a chunk");
     add_to_state(0);
-    if constexpr (KT == 2) {
-      read_k(1, 0, 8);
-      weigh_values(1);
-      __builtin_amdgcn_sched_barrier(0);
+    weigh_values(1);
+    if constexpr (MSV == NSV) read_k(1, 0, 8);
+    if constexpr (BF) {
+#pragma unroll
+      for (int i = 0; i < 8 * MSV; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        if (MSV == NSV && i >= 8 * (NSV - 1)) __builtin_amdgcn_sched_group_barrier(0x100, Tok<E>::READS, 0);
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    add_rest(0);
+    if constexpr (MSV < NSV) read_k(1, 0, 8);
     if constexpr (OUT) {
       // rows behind the end fall outside the buffer view and are dropped
       const Rsrc orb = make_rsrc(static_cast<char*>(p.o) + ((size_t)t0 * H + h) * (D * oes),
@@ -1040,9 +1059,8 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
         }
       }
     }
-    if constexpr (KT == 2) add_to_state(1);
-    // the next chunk's queries: its tiles are in LDS already (the last chunk
-    // reads what is there and drops it)
+    add_to_state(1);
+    add_rest(1);
     read_q(base_next, 0);
     read_q(base_next, 1);
     base = base_next;
