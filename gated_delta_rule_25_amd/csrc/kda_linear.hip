@@ -892,24 +892,25 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     // The LDS reads run a few operands ahead of the products, in the order of
     // use (at most 15 can be waited for one by one); the vector arithmetic
     // fills the gaps between products.
+    if (NW == 8 && wv >= 4) __builtin_amdgcn_s_setprio(1);
     const uint32_t base_next = base + L::SET == lds0 + NBUF * L::SET ? lds0 : base + L::SET;
     const uint32_t vbase = lds0 + L::VALS + (ci & 1) * L::VTILE;
     const float gam = sGam[b];
     float w[KT][TN];
     TF fv[KT], fk[8];
-    auto read_values = [&]() {
+    auto read_values = [&](int kt) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
+      for (int i = 0; i < TN; i += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + 4 * TN * kt + TN * g + i);
 #pragma unroll
-        for (int i = 0; i < TN; i += 4) {
-          const f32x4 y = *reinterpret_cast<const f32x4*>(sWgt + b * C + 4 * TN * kt + TN * g + i);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
-        }
-        ld_col(fv[kt], vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
+        for (int j = 0; j < 4; ++j) w[kt][i + j] = y[j];
       }
+      ld_col(fv[kt], vbase + kt * (4 * TN * L::VW * ES), v_at, 0);
     };
-    if constexpr (!DG) read_values();
+    if constexpr (!DG) {
+      read_values(0);
+      read_values(1);
+    }
     auto read_k = [&](int kt, int first, int count) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt)
@@ -959,6 +960,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       for (int ks = 0; ks < 4; ++ks) {
         if (ks == 0) split_state(0);
         if (ks < 3) split_state(ks + 1);
+        if (DG && ks == 3) read_values(0);
 #pragma unroll
         for (int s = 0; s < NSS; ++s)
 #pragma unroll
@@ -976,7 +978,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (DG) {  // (no registers for them earlier)
-        read_values();
+        read_values(1);
         read_k(0, 0, 4);
       }
       weigh_values(0);
@@ -1019,6 +1021,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       read_k(0, 0, 8);
       weigh_values(0);
     }
+    if (NW == 8 && wv >= 4) __builtin_amdgcn_s_setprio(0);
     // the state's scale, when the decays have run far enough (decay wave)
     if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gam)) != 0x3f800000) {
 #pragma unroll
@@ -1075,36 +1078,41 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   }
 }
 
-// Blocks b and b + 8 run on the same XCD: what the blocks of one work item
-// (PER of them) both read comes from its L2 the second time.
-template <int PER>
-__device__ __forceinline__ int64_t work_item(int& part) {
-  const int64_t slot8 = blockIdx.x >> 3;
-  part = (int)(slot8 % PER);
-  return (slot8 / PER) * 8 + (blockIdx.x & 7);
-}
-
 template <typename E, int NW, bool REV, bool OUT>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  int cb;
-  const int64_t u = work_item<8 / NW>(cb);
+  // Blocks b and b + 8 run on the same XCD: what a head's column blocks both
+  // read comes from its L2 the second time.
+  constexpr int CB = 8 / NW;
+  const int64_t slot8 = blockIdx.x >> 3, u = slot8 / CB * 8 + (blockIdx.x & 7);
+  const int cb = (int)(slot8 % CB);
   if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, cb);
 }
 
-// The three gradients' walks of every work item, side by side.  The walks that
-// go backwards read the same tensors at about the same time.
+// The three gradients' walks of every work item: per sequence (or segment) the
+// dq and dk walks of all heads, which take longer, then the dv walks.
 template <typename E, int NW, bool DG>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_grad_kernel(const LinearGradArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int CB = 8 / NW;
-  int part;
-  const int64_t u = work_item<3 * CB>(part);
-  if (u >= p.dq.units) return;
+  const int H = p.dq.num_heads, H8 = (H + 7) / 8 * 8;
+  const int per = 3 * CB * H8;  // blocks of an item; b and b + 8 run on the same XCD
+  const int64_t item = blockIdx.x / per;
+  const int at = blockIdx.x % per, slot8 = at >> 3;
+  int part, h;
+  if (at < 2 * CB * H8) {
+    part = slot8 % (2 * CB);
+    h = slot8 / (2 * CB) * 8 + (at & 7);
+  } else {
+    part = slot8 % CB + 2 * CB;
+    h = (slot8 - 2 * CB * (H8 / 8)) / CB * 8 + (at & 7);
+  }
+  if (h >= H) return;
+  const int64_t u = item * H + h;
   const int cb = part % CB;
   if (part < CB) walk<E, NW, true, true, true, DG>(p.dk, smem, u, cb);
-  else if (part < 2 * CB) walk<E, NW, true, false, true, false>(p.dv, smem, u, cb);
-  else walk<E, NW, false, true, true, DG>(p.dq, smem, u, cb);
+  else if (part < 2 * CB) walk<E, NW, false, true, true, DG>(p.dq, smem, u, cb);
+  else walk<E, NW, true, false, true, false>(p.dv, smem, u, cb);
 }
 
 // Dynamic LDS above 64 KiB has to be asked for, once per device.
@@ -1144,7 +1152,7 @@ hipError_t launch_grad_t(const LinearGradArgs& a, hipStream_t stream) {
   static std::atomic<bool> set[64];
   hipError_t e = allow_lds(linear_grad_kernel<E, NW, DG>, LDS, set);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (a.dq.units + 7) / 8 * 8 * 3 * (8 / NW);
+  const int64_t H = a.dq.num_heads, blocks = a.dq.units / H * ((H + 7) / 8 * 8) * 3 * (8 / NW);
   hipLaunchKernelGGL((linear_grad_kernel<E, NW, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
   return hipGetLastError();
 }

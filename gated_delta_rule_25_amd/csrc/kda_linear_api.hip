@@ -46,34 +46,43 @@ struct LinearPlan {
   size_t bytes = 0;
 };
 
-// Whether sequences are cut into segments that run side by side, and how
-// long those are.  One workgroup fills a compute unit, so a walk per
-// (sequence, head) leaves units idle when there are fewer chains than units;
-// segments cost a pass for their contributions (two in the backward pass) and
-// their states' traffic.  Forward: from three units per chain on, one segment
-// per unit (8 heads x 131072 tokens: 380 us in segments of 4096 against 448 at
-// 1024 and 3726 us in one walk; 96 heads x 8192: 280 us in one walk of half
-// heads against 330 at 1024).  Backward, three walks: whenever chains are
-// fewer than units, three segments per unit, of 512 tokens at least (96 heads
-// x 8192: 1036 us in segments of 1024 against 1573 in one walk; 9 ragged
-// sequences of 4927 tokens x 16 heads: 202 us at 512, 229 at 256, 560 in one).
+// Whether sequences are cut into segments that run side by side and how long
+// those are, and whether a walk takes half a head.  One workgroup fills a
+// compute unit, so a walk per (sequence, head) leaves units idle when there are
+// fewer chains than units; segments cost a pass for their contributions (two in
+// the backward pass) and their states' traffic; half heads cost a second copy
+// of the pair matrix but make a chain shorter (3.4 us per chunk of the dq walk
+// against 4.7).
+//
+// Forward: segments, one per unit, from three units per chain on (8 heads x
+// 131072 tokens: 380 us in segments of 4096, 448 at 1024, 3726 in one walk; 96
+// heads x 8192: 225 us in one walk of half heads, 300 at 1536); half heads
+// when chains are fewer than units.
+// Backward, three walks a chain: segments, one per unit, from six units per
+// chain on (32 heads x 8192 tokens: 308 us in segments of 1024, 345 at 512,
+// 359 in one walk of half heads, 443 of whole ones; 48 heads: 477, 508, 489,
+// 495).  With more chains one walk each: whole heads if all chains are as long
+// (96 heads x 8192: 757-847 us, half heads 975, segments of 1024 870).  The
+// lengths of several sequences are not known here, and the longest one is
+// waited for: half heads until two rounds of the card are full (9 sequences of
+// up to 2900 tokens x 16 heads: 157 us, whole heads 206; of up to 1200: 103
+// against 85).
 void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
                      bool backward) {
   const int64_t units = (int64_t)num_seqs * num_heads;
-  pl.narrow = units < cus;
+  const bool few = (backward ? 6 : 3) * units < cus;
   if (segment_tokens > 0) {
     pl.segmented = true;
     pl.seg = segment_tokens;
-  } else if (segment_tokens == 0 && (backward ? 6 : 3) * units < cus) {
-    const int64_t target = (int64_t)cus * (backward ? 3 : 1);
-    int64_t seg = (total_tokens * num_heads + target - 1) / target;
+  } else if (segment_tokens == 0 && few) {
+    int64_t seg = (total_tokens * num_heads + cus - 1) / cus;
     seg = std::max((seg + 255) / 256 * 256, kMinSegment);
     if ((int64_t)num_seqs * seg < total_tokens) {
       pl.segmented = true;
       pl.seg = seg;
     }
   }
-  if (pl.segmented) pl.narrow = false;
+  if (!pl.segmented) pl.narrow = backward ? few || (num_seqs > 1 && 3 * units < 2 * cus) : units < cus;
   pl.slots = kda::linear_slots(total_tokens, num_seqs, pl.seg);
 }
 
