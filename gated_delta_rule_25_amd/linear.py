@@ -64,8 +64,11 @@ def _sizes(q, k, v, log_decay, cu_seqlens, lead):
 
 
 def _workspace(workspace, need, dev):
-    if workspace is not None and workspace.device != dev:
-        raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+        if not workspace.is_contiguous():  # (an expanded tensor has less memory than elements)
+            raise ValueError("workspace must be contiguous")
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -168,6 +171,20 @@ def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     return dq, dk, dv, dg, ds
 
 
+_STREAM = "chunk_linear.stream"
+
+
+def _mark_accumulators(out: torch.Tensor) -> None:
+    """Notes on the leaves' gradient accumulators the stream they were made on.
+    One lives as long as some graph of its leaf, and a captured backward whose
+    accumulator belongs to a stream outside the capture ends the process."""
+    if out.grad_fn is not None:
+        stream = torch.cuda.current_stream(out.device).cuda_stream
+        for node, _ in out.grad_fn.next_functions:
+            if hasattr(node, "variable"):
+                node.metadata.setdefault(_STREAM, stream)
+
+
 class _ChunkLinear(torch.autograd.Function):
     """linear_chunk_fwd forward, linear_chunk_bwd backward (which needs only
     the forward's inputs)."""
@@ -180,7 +197,15 @@ class _ChunkLinear(torch.autograd.Function):
         return o, final_state
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, d_final_state):
+        if torch.cuda.is_current_stream_capturing():
+            stream = torch.cuda.current_stream().cuda_stream
+            for node, _ in ctx.next_functions:
+                if hasattr(node, "variable") and node.metadata.get(_STREAM, stream) != stream:
+                    raise RuntimeError("chunk_linear: a gradient is accumulated by a node that was made outside the "
+                                       "graph capture; free the outputs of earlier eager calls with the same leaves, "
+                                       "and capture the forward with the backward")
         q, k, v, log_decay, initial_state, cu_seqlens = ctx.saved_tensors
         d_o = torch.zeros_like(v) if d_o is None else d_o.to(v.dtype).contiguous()
         if d_final_state is not None:
@@ -197,8 +222,13 @@ def chunk_linear(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
                  cu_seqlens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable prefill (torch.autograd): (o, final_state) as
     linear_chunk_fwd, with gradients for q, k, v, log_decay (when it requires
-    one) and the initial state from linear_chunk_bwd."""
-    return _ChunkLinear.apply(q, k, v, log_decay, initial_state, cu_seqlens)
+    one) and the initial state from linear_chunk_bwd, once (no gradients of
+    gradients).  A graph capture has to hold the forward and the backward, with
+    no output of an eager call with the same leaves alive: a backward that
+    would accumulate through such a call's nodes is refused."""
+    o, final_state = _ChunkLinear.apply(q, k, v, log_decay, initial_state, cu_seqlens)
+    _mark_accumulators(o)
+    return o, final_state
 
 
 def linear_decode_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
