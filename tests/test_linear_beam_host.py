@@ -1,0 +1,245 @@
+"""Host-side checks of include/kda_linear.h and include/kda_beam.h (no GPU
+needed, nothing is launched): the library exports what the headers declare,
+the workspace queries, and refusals.  Every call here is built to fail its
+validation; the addresses are made up and never dereferenced."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import gated_delta_rule_25_amd as kda
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+F32, BF16 = 0, 1
+MIB = 1 << 20
+BASE = 0x7F0000000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda._LIB_PATH):
+        from gated_delta_rule_25_amd import build
+        build.build()
+    return kda._load()
+
+
+def p(i, off=0):
+    return ctypes.c_void_p(BASE + i * 64 * MIB + off)
+
+
+@pytest.mark.parametrize("header", ["kda_linear.h", "kda_beam.h"])
+def test_header_symbols_exported(lib, header):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
+    names = set(re.findall(r"\b(kda_[a-z_]+)\s*\(", text))
+    assert len(names) >= 3
+    out = subprocess.run(["nm", "-D", "--defined-only", kda._LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (kda_[a-z_]+)$", out, flags=re.M))
+
+
+@pytest.mark.parametrize("header", ["kda_linear.h", "kda_beam.h"])
+def test_headers_are_c(header, tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text("#include \"%s\"\nint main(void) { return 0; }\n" % header)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"),
+                    "-I", "/opt/rocm/include", "-fsyntax-only", str(src)], check=True)
+
+
+def fwd(lib, **kw):
+    a = dict(q=p(0), k=p(1), v=p(2), la=p(3), s0=None, cu=None, N=1, T=10, H=4, Hq=2, ph=0, dk=128, dv=128, dt=BF16,
+             seg=0, o=p(5), fs=p(6), ws=p(8), wsb=32 * MIB)
+    a.update(kw)
+    return lib.kda_linear_chunk_fwd(a["q"], a["k"], a["v"], a["la"], a["s0"], a["cu"], a["N"], a["T"], a["H"], a["Hq"],
+                                    a["ph"], a["dk"], a["dv"], a["dt"], a["seg"], a["o"], a["fs"], a["ws"], a["wsb"],
+                                    None)
+
+
+def bwd(lib, **kw):
+    a = dict(q=p(0), k=p(1), v=p(2), la=p(3), s0=None, cu=None, do=p(4), dfs=None, N=1, T=10, H=4, Hq=2, ph=0, dk=128,
+             dv=128, dt=BF16, seg=0, oq=p(5), ok=p(6), ov=p(7), og=p(9), os=p(10), ws=p(8), wsb=64 * MIB)
+    a.update(kw)
+    return lib.kda_linear_chunk_bwd(a["q"], a["k"], a["v"], a["la"], a["s0"], a["cu"], a["do"], a["dfs"], a["N"], a["T"],
+                                    a["H"], a["Hq"], a["ph"], a["dk"], a["dv"], a["dt"], a["seg"], a["oq"], a["ok"],
+                                    a["ov"], a["og"], a["os"], a["ws"], a["wsb"], None)
+
+
+BOTH = pytest.mark.parametrize("call", [fwd, bwd], ids=["fwd", "bwd"])
+
+
+@BOTH
+@pytest.mark.parametrize("kw,status", [
+    (dict(dk=64), UNSUPPORTED), (dict(dv=256), UNSUPPORTED), (dict(dt=7), UNSUPPORTED),
+    (dict(N=0), INVALID), (dict(H=0), INVALID), (dict(Hq=0), INVALID), (dict(T=-1), INVALID),
+    (dict(H=4, Hq=3), INVALID), (dict(H=2, Hq=4), INVALID), (dict(H=65536, Hq=1), INVALID),
+    (dict(T=1 << 31), INVALID),                              # more tokens than cu_seqlens can count
+    (dict(N=2), INVALID),                                    # several sequences need cu_seqlens
+    (dict(seg=63), INVALID), (dict(seg=100), INVALID),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(la=None), INVALID),
+    (dict(q=p(0, 8)), INVALID), (dict(v=p(2, 4)), INVALID), (dict(s0=p(11, 8)), INVALID), (dict(ws=p(8, 8)), INVALID),
+    (dict(la=p(3, 2)), INVALID), (dict(N=2, cu=p(7, 2)), INVALID),
+    (dict(seg=64, T=1000, ws=None), WORKSPACE), (dict(seg=64, T=1000, wsb=16), WORKSPACE),
+    (dict(seg=64, T=1000, ws=p(0)), INVALID),                # workspace over q
+])
+def test_chunk_refusals(lib, call, kw, status):
+    assert call(lib, **kw) == status
+
+
+def test_fwd_refusals(lib):
+    assert fwd(lib, o=None) == INVALID
+    assert fwd(lib, o=p(0)) == INVALID                       # the output over q, over the states
+    assert fwd(lib, o=p(6)) == INVALID
+    assert fwd(lib, s0=p(5)) == INVALID
+    assert fwd(lib, fs=p(3)) == INVALID
+    assert fwd(lib, fs=p(6, 8)) == INVALID                   # not 16-byte aligned
+    assert fwd(lib, s0=p(6, 64), fs=p(6)) == INVALID         # neither the same state nor another
+    assert fwd(lib, N=2, cu=p(6)) == INVALID                 # the final state over cu_seqlens
+
+
+def test_bwd_refusals(lib):
+    for name in ("do", "oq", "ok", "ov"):
+        assert bwd(lib, **{name: None}) == INVALID, name
+    outs = ("oq", "ok", "ov", "og", "os")
+    for i, name in enumerate(outs):
+        for at in (0, 1, 2, 3, 4):                           # over an input
+            assert bwd(lib, **{name: p(at)}) == INVALID, (name, at)
+        for other in outs[i + 1:]:                           # over another output
+            assert bwd(lib, **{name: p(12), other: p(12)}) == INVALID, (name, other)
+        assert bwd(lib, **{name: p(8)}) == INVALID, name     # over the workspace
+    assert bwd(lib, s0=p(10)) == INVALID                     # states are not updated in place here
+    assert bwd(lib, dfs=p(10)) == INVALID
+    assert bwd(lib, og=p(9, 2)) == INVALID
+    assert bwd(lib, os=p(10, 4)) == INVALID
+    assert bwd(lib, wsb=16) == WORKSPACE                     # shared heads are summed from the workspace
+
+
+def test_chunk_workspaces(lib):
+    f, b = lib.kda_linear_chunk_fwd_workspace_bytes, lib.kda_linear_chunk_bwd_workspace_bytes
+    state = 128 * 128 * 4
+    assert f(1, 1000, 4, 2, 128, 128, BF16, -1) == 0
+    # slots 1000 // 64 + 2 of 4 states, and the segments' decays
+    assert f(1, 1000, 4, 2, 128, 128, BF16, 64) == 17 * 4 * state + 512
+    assert f(1, 1000, 4, 2, 128, 128, BF16, 63) == 0
+    assert f(0, 1000, 4, 2, 128, 128, BF16, 64) == 0
+    assert f(1, 1000, 4, 3, 128, 128, BF16, 64) == 0
+    assert f(1, 1000, 4, 2, 64, 128, BF16, 64) == 0
+    assert f(1, 1000, 4, 2, 128, 128, 9, 64) == 0
+    assert f(1, 1 << 31, 4, 2, 128, 128, BF16, 64) == 0
+    # backward without the decays' gradient: the states of both directions, decays, and the shared heads' fp32 sums
+    assert b(1, 1000, 4, 4, 0, 0, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512
+    assert b(1, 1000, 4, 2, 0, 0, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512 + 2 * 1000 * 4 * 128 * 4
+    assert b(1, 1000, 4, 4, 0, 0, 128, 128, BF16, -1) == 0
+    assert b(1, 1000, 4, 4, 0, 1, 128, 128, BF16, -1) > 0
+    # a segment length with a large prime factor is cut at every 64 tokens
+    assert b(1, 200000, 1, 1, 0, 1, 128, 128, BF16, 64 * 1021) > 2 * 3125 * state
+
+
+def decode(lib, **kw):
+    a = dict(S=p(0), q=p(1), k=p(2), v=p(3), la=p(4), N=3, H=4, Hq=2, ph=0, dk=128, dv=128, dt=BF16, o=p(5))
+    a.update(kw)
+    return lib.kda_linear_decode_step(a["S"], a["q"], a["k"], a["v"], a["la"], a["N"], a["H"], a["Hq"], a["ph"], a["dk"],
+                                      a["dv"], a["dt"], a["o"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dk=64), UNSUPPORTED), (dict(dv=64), UNSUPPORTED), (dict(dt=5), UNSUPPORTED),
+    (dict(N=0), INVALID), (dict(H=0), INVALID), (dict(Hq=3), INVALID), (dict(H=70000, Hq=1), INVALID),
+    (dict(S=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(la=None), INVALID), (dict(o=None), INVALID), (dict(S=p(0, 8)), INVALID),
+    (dict(o=p(0)), INVALID), (dict(o=p(1)), INVALID), (dict(o=p(4)), INVALID), (dict(q=p(0, 256)), INVALID),
+])
+def test_decode_refusals(lib, kw, status):
+    assert decode(lib, **kw) == status
+
+
+def select(lib, **kw):
+    a = dict(x=p(0), s=p(1), f=None, B=2, K=4, V=1000, end=0, dt=BF16, os=p(2), ot=p(3), op=p(4), of=None, ws=p(6),
+             wsb=16 * MIB)
+    a.update(kw)
+    return lib.kda_beam_select(a["x"], a["s"], a["f"], a["B"], a["K"], a["V"], a["end"], a["dt"], a["os"], a["ot"],
+                               a["op"], a["of"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), INVALID), (dict(K=0), INVALID), (dict(V=0), INVALID), (dict(K=17), UNSUPPORTED),
+    (dict(dt=9), UNSUPPORTED), (dict(B=1 << 30, K=16), INVALID),
+    (dict(x=None), INVALID), (dict(s=None), INVALID), (dict(os=None), INVALID), (dict(ot=None), INVALID),
+    (dict(op=None), INVALID), (dict(f=p(7)), INVALID), (dict(of=p(7)), INVALID),
+    (dict(f=p(7), of=p(9), end=-1), INVALID), (dict(f=p(7), of=p(9), end=1000), INVALID),
+    (dict(x=p(0, 1)), INVALID), (dict(x=p(0, 2), dt=F32), INVALID), (dict(os=p(2, 2)), INVALID),
+    (dict(ws=p(6, 8)), INVALID), (dict(ws=None), WORKSPACE), (dict(wsb=64), WORKSPACE),
+    (dict(os=p(0)), INVALID), (dict(ot=p(1)), INVALID), (dict(op=p(3)), INVALID), (dict(ws=p(0)), INVALID),
+    (dict(os=p(1, 4)), INVALID), (dict(f=p(7), of=p(7, 1)), INVALID), (dict(f=p(7), of=p(2)), INVALID),
+])
+def test_select_refusals(lib, kw, status):
+    assert select(lib, **kw) == status
+
+
+def test_select_workspace(lib):
+    w = lib.kda_beam_select_workspace_bytes
+    assert w(0, 4, 100, BF16) == 0 and w(1, 17, 100, BF16) == 0 and w(1, 4, 0, BF16) == 0 and w(1, 4, 100, 9) == 0
+    assert 0 < w(1, 4, 100, BF16) <= w(1, 4, 128003, BF16) < w(64, 8, 128003, F32)
+    assert w(1, 1, (1 << 31) - 1, BF16) > 0  # the longest row
+
+
+def reorder(lib, states, rows, n=None, parents=p(9), B=2, K=4):
+    ptrs = (ctypes.c_void_p * max(1, len(states)))(*states)
+    by = (ctypes.c_int64 * max(1, len(rows)))(*rows)
+    return lib.kda_beam_reorder(ptrs, by, len(states) if n is None else n, parents, B, K, None)
+
+
+def test_reorder_refusals(lib):
+    s = [p(0), p(1)]
+    assert reorder(lib, s, [64, 64], B=0) == INVALID
+    assert reorder(lib, s, [64, 64], K=0) == INVALID
+    assert reorder(lib, s, [64, 64], K=17) == UNSUPPORTED
+    assert reorder(lib, s, [64, 64], n=9) == UNSUPPORTED
+    assert reorder(lib, s, [64, 64], n=0) == INVALID
+    assert reorder(lib, s, [64, 64], parents=None) == INVALID
+    assert reorder(lib, s, [64, 64], parents=p(9, 2)) == INVALID
+    assert reorder(lib, [p(0), None], [64, 64]) == INVALID
+    assert reorder(lib, s, [64, -1]) == INVALID
+    assert reorder(lib, s, [64, 1 << 62]) == INVALID
+    assert reorder(lib, [p(0), p(0)], [64, 64]) == INVALID          # the same tensor twice
+    assert reorder(lib, [p(0), p(0, 256)], [64, 64]) == INVALID     # two that overlap
+    assert reorder(lib, [p(0), p(9)], [64, 64]) == INVALID          # parents among the states
+    assert lib.kda_beam_reorder(None, None, 1, p(9), 2, 4, None) == INVALID
+
+
+# ---- the Python entry points refuse before they reach the library ----------
+
+def cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_python_refusals():
+    q, v, la = cpu(5, 2, 128), cpu(5, 4, 128), cpu(5, 4, dtype=torch.float32)
+    S = cpu(5, 4, 128, 128, dtype=torch.float32)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.linear_chunk_fwd(q, q, v, la)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.linear_decode_step(S, q, q, v, la)
+    with pytest.raises(ValueError, match="Hq, 128"):
+        kda.linear_chunk_fwd(cpu(5, 2, 64), q, v, la)
+    with pytest.raises(ValueError, match="H, 128"):
+        kda.linear_chunk_fwd(q, q, cpu(5, 512), la)
+    with pytest.raises(ValueError, match="multiple"):
+        kda.linear_chunk_fwd(cpu(5, 3, 128), cpu(5, 3, 128), v, la)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        kda.linear_chunk_fwd(q.half(), q.half(), v.half(), la)
+    with pytest.raises(TypeError, match="k must be a torch.Tensor"):
+        kda.linear_chunk_fwd(q, None, v, la)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.beam_select(cpu(2, 4, 10), cpu(2, 4, dtype=torch.float32))
+    with pytest.raises(ValueError, match="B, K, V"):
+        kda.beam_select(cpu(4, 10), cpu(4, dtype=torch.float32))
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        kda.beam_select(cpu(2, 4, 10).half(), cpu(2, 4, dtype=torch.float32))
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.beam_reorder(S, cpu(1, 5, dtype=torch.int32))
+    with pytest.raises(ValueError, match="B, K"):
+        kda.beam_reorder(S, cpu(5, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        kda.beam_reorder(S, [0, 1])
