@@ -11,20 +11,26 @@ every tensor that holds something per sequence.  One step of the search:
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import KDA_OK, KDAError, _check, _DTYPES, _load, _ptr, _stream
-from .linear import _on, _workspace
+from . import KDA_OK, KDAError, _check, _DTYPES, _load
+from .linear import _on, _ptr, _stream, _workspace
 
 BEAM_MAX = 16
 BEAM_REORDER_MAX = 8
 
 
+@functools.lru_cache(maxsize=64)
+def _select_bytes(groups: int, beams: int, vocab: int, dtype: int) -> int:
+    return int(_load().kda_beam_select_workspace_bytes(groups, beams, vocab, dtype))
+
+
 def beam_select_workspace_bytes(groups: int, beams: int, vocab: int, dtype: torch.dtype = torch.bfloat16) -> int:
     """Workspace bytes of beam_select."""
-    return int(_load().kda_beam_select_workspace_bytes(groups, beams, vocab, _DTYPES[dtype]))
+    return _select_bytes(groups, beams, vocab, _DTYPES[dtype])
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[torch.Tensor] = None, *,
@@ -73,8 +79,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     else:
         _check(new_finished, "out finished", (b, k), torch.bool, dev)
     with _on(dev):
-        need = int(lib.kda_beam_select_workspace_bytes(b, k, v, _DTYPES[dt]))
-        workspace, ws_bytes = _workspace(workspace, need, dev)
+        workspace, ws_bytes = _workspace(workspace, _select_bytes(b, k, v, _DTYPES[dt]), dev)
         rc = lib.kda_beam_select(_ptr(logits), _ptr(scores), _ptr(finished), b, k, v,
                                  0 if finished is None else int(end_token), _DTYPES[dt], _ptr(new_scores),
                                  _ptr(tokens), _ptr(parents), _ptr(new_finished), _ptr(workspace), ws_bytes,
@@ -108,20 +113,21 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     for t in many:
         if not isinstance(t, torch.Tensor):
             raise TypeError("states must be torch.Tensors")
-        if tuple(t.shape[:1]) != (b * k,) and tuple(t.shape[:2]) != (b, k):
+        if t.shape[:1] != (b * k,) and t.shape[:2] != (b, k):
             raise ValueError("a state has shape %s, expected [%d, ...] or [%d, %d, ...]" % (tuple(t.shape), b * k, b, k))
         if t.device != dev:
             raise ValueError("a state is on %s, expected %s" % (t.device, dev))
         if not t.is_contiguous():
             raise ValueError("states must be contiguous")
-    held = [t.data_ptr() for t in many if t.numel()]
-    if len(set(held)) != len(held):
-        raise ValueError("the same state is given twice")
+    if len(many) > 1:
+        held = [t.data_ptr() for t in many if t.numel()]
+        if len(set(held)) != len(held):
+            raise ValueError("the same state is given twice")
     with _on(dev):
         for i in range(0, len(many), BEAM_REORDER_MAX):
             part = many[i:i + BEAM_REORDER_MAX]
-            ptrs = (ctypes.c_void_p * len(part))(*(t.data_ptr() for t in part))
-            rows = (ctypes.c_int64 * len(part))(*(t.numel() * t.element_size() // (b * k) if b * k else 0 for t in part))
+            ptrs = (ctypes.c_void_p * len(part))(*[t.data_ptr() for t in part])
+            rows = (ctypes.c_int64 * len(part))(*[t.nbytes // (b * k) if b * k else 0 for t in part])
             rc = lib.kda_beam_reorder(ptrs, rows, len(part), _ptr(parents), b, k, _stream(dev))
             if rc != KDA_OK:
                 raise KDAError(rc, "kda_beam_reorder")

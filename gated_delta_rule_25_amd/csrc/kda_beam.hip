@@ -19,8 +19,8 @@
 //                      Bound by HBM.
 //   beam_pick_kernel   one workgroup per group: the K best parts of each row,
 //                      their elements read again (K x nv vectors), the row's
-//                      K best; then one wave takes the K best of the K x K
-//                      candidates, compared as fp64 scores.
+//                      K best; then the K best of the K x K candidates,
+//                      compared as fp64 scores.
 // Nothing depends on the order in which workgroups run.
 //
 // Reordering.  Row n of a group's states becomes the row of its parent.  A
@@ -69,15 +69,6 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t x) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), 63);
   return (uint64_t)hi << 32 | lo;
 }
-// an fp64 number as an integer of the same order
-__device__ __forceinline__ uint64_t double_key(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
-  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
-}
-__device__ __forceinline__ double key_double(uint64_t k) {
-  return __builtin_bit_cast(double, (k >> 63) ? k ^ 0x8000000000000000ull : ~k);
-}
-
 // NaN is a masked logit like -inf (the maximum of NaN and a number is the
 // number); +inf counts as the largest finite number.
 __device__ __forceinline__ float beam_logit(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
@@ -237,14 +228,14 @@ __device__ __forceinline__ float wave_fmax(float x) {
 // One workgroup per group, wave k for beam k.
 //   1. The C = min(K, V) best parts.  A lane holds up to 32; the C-th largest
 //      of the lanes' own maxima is a bound that at least C parts reach, and
-//      seldom many more: those move to one a lane, where C rounds of the
-//      wave's maximum sort them out.  (Ties beyond 64 parts take the rounds
-//      over all parts.)
+//      seldom many more: those move to one a lane and are sorted by counting.
+//      (More than 64, which takes ties, go through C rounds of the wave's
+//      maximum over all parts.)
 //   2. Their largest elements are C elements of the row, so none below the
 //      last of them is wanted.
 //   3. The C parts are read again; where one holds another element that is
 //      wanted (seldom), the list of the C best is formed anew with it.
-// Then one wave takes the K best of the K x C candidates.
+// Then the waves place the K x C candidates by counting as well.
 template <typename E>
 __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSelectArgs a) {
   constexpr int U = 16 / (int)sizeof(E);
@@ -326,16 +317,29 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
       uint64_t list = 0;  // lane i < C: the i-th best element
       int part = -1;      // and the part it is from
       uint64_t least = 0;
-      uint64_t cur = 0;
-      int id = -1;
-      if (few <= 64 && lane < few) {
-        cur = few_key[k][lane];
-        id = few_id[k][lane];
-      }
-      uint64_t before = ~0ull;
-      for (int c = 0; c < C; ++c) {
-        if (few > 64) {
-          cur = 0;
+      if (few <= 64) {
+        // sorted by counting: a part's place is the number of better ones
+        // (their keys differ, as the indices do)
+        const uint64_t cur = lane < few ? few_key[k][lane] : 0;
+        const int id = lane < few ? few_id[k][lane] : -1;
+        int place = 0;
+        for (int j = 0; j < few; ++j) place += few_key[k][j] > cur;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (lane < few) {
+          few_key[k][place] = cur;
+          few_id[k][place] = id;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (lane < min(few, C)) {
+          list = few_key[k][lane];
+          part = few_id[k][lane];
+        }
+        if (few >= C) least = __shfl((unsigned long long)list, C - 1);
+      } else {
+        uint64_t before = ~0ull;
+        for (int c = 0; c < C; ++c) {
+          uint64_t cur = 0;
+          int id = -1;
 #pragma unroll
           for (int i = 0; i < PL; ++i) {
             const uint64_t key = where[i] != INT32_MAX ? beam_key(top[i], (uint32_t)where[i]) : 0;
@@ -344,18 +348,15 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
               id = 64 * i + lane;
             }
           }
+          const uint64_t w = wave_max(cur);
+          const int src = __ffsll((unsigned long long)__ballot(cur == w)) - 1;
+          const int got = __builtin_amdgcn_readlane(id, src);
+          if (lane == c) {
+            list = w;
+            part = got;
+          }
+          before = least = w;
         }
-        const uint64_t w = wave_max(cur);
-        if (w == 0) break;  // fewer parts than candidates
-        const int src = __ffsll((unsigned long long)__ballot(cur == w)) - 1;
-        const int got = __builtin_amdgcn_readlane(id, src);
-        if (lane == c) {
-          list = w;
-          part = got;
-        }
-        if (cur == w) cur = 0;
-        before = w;
-        if (c == C - 1) least = w;
       }
       // their elements: vector j of part i is lane i nv + j (64 a turn)
       const E* x = static_cast<const E*>(a.logits) + row * V;
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
             if (key[j] == have) key[j] = 0;
         }
         uint64_t keep = 0;
-        before = ~0ull;
+        uint64_t before = ~0ull;
         for (int c = 0; c < C; ++c) {
           uint64_t b = list < before ? list : 0;
 #pragma unroll
@@ -424,40 +425,30 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
     if (lane == 0) done[k] = fin;
   }
   __syncthreads();
-  if (k != 0) return;
-  // the K best of the K x C candidates (C = K, or V < K candidates a row):
-  // the largest score, then the lowest index with it
-  constexpr int CL = kBeamMax * kBeamMax / 64;
-  uint64_t sk[CL], ak[CL];
-#pragma unroll
-  for (int i = 0; i < CL; ++i) {
-    sk[i] = ak[i] = 0;
-    if (lane + 64 * i < K * C) {
-      sk[i] = double_key(cand_score[lane + 64 * i]);
-      ak[i] = ~cand_at[lane + 64 * i];
-    }
+  // the K best of the K x C candidates (C = K, or V < K candidates a row): a
+  // candidate's place is the number of better ones, the largest score first,
+  // then the lowest index with it.  Wave k places its own row's, each by 8
+  // lanes (4 with more than 8 beams).
+  const int sh = K > 8 ? 2 : 3, lanes = 1 << sh;
+  const int c = lane >> sh;
+  const int me = k * C + min(c, C - 1);
+  const double ms = cand_score[me];
+  const uint64_t ma = cand_at[me];
+  int place = 0;
+  for (int j = lane & (lanes - 1); j < K * C; j += lanes) {
+    const double s = cand_score[j];
+    const uint64_t t = cand_at[j];
+    place += s > ms || (s == ms && (t < ma || (t == ma && j < me)));
   }
-  for (int c = 0; c < K; ++c) {
-    uint64_t s = 0, t = 0;
-#pragma unroll
-    for (int i = 0; i < CL; ++i) s = sk[i] > s ? sk[i] : s;
-    s = wave_max(s);
-#pragma unroll
-    for (int i = 0; i < CL; ++i) t = sk[i] == s && ak[i] > t ? ak[i] : t;
-    t = wave_max(t);
-#pragma unroll
-    for (int i = 0; i < CL; ++i)
-      if (ak[i] == t) sk[i] = ak[i] = 0;
-    if (lane == 0) {
-      // (K V >= K candidates always exist; the clamps keep a wrong one in range)
-      const int parent = min((int)(~t >> 32 & 0xffffu), K - 1);
-      const int token = min((uint32_t)~t, (uint32_t)(V - 1));
-      const int64_t o = (int64_t)g * K + c;
-      a.out_scores[o] = (float)key_double(s);
-      a.out_tokens[o] = token;
-      a.out_parents[o] = parent;
-      if (a.out_finished) a.out_finished[o] = done[parent] || token == a.end_token;
-    }
+  for (int m = lanes >> 1; m >= 1; m >>= 1) place += __shfl_xor(place, m);
+  if (c < C && (lane & (lanes - 1)) == 0 && place < K) {
+    // (the clamp keeps a wrong candidate in range)
+    const int token = (int)min((uint32_t)ma, (uint32_t)(V - 1));
+    const int64_t o = (int64_t)g * K + place;
+    a.out_scores[o] = (float)ms;
+    a.out_tokens[o] = token;
+    a.out_parents[o] = k;
+    if (a.out_finished) a.out_finished[o] = done[k] || token == a.end_token;
   }
 }
 

@@ -19,14 +19,29 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import D, KDA_OK, KDAError, _check, _DTYPES, _load, _ptr, _stream
+from . import D, KDA_OK, KDAError, _check, _DTYPES, _load
+
+
+# The calls for single tokens take a few microseconds on the GPU, so what the
+# host does for each counts: addresses and the stream go to ctypes as plain
+# integers, the latter without a torch.cuda.Stream around it.
+_HERE = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(dev: torch.device):
     """The kernels run on the tensors' device, whichever is current."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream(dev: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _sizes(q, k, v, log_decay, cu_seqlens, lead):
