@@ -1090,29 +1090,37 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
 }
 
 // The three gradients' walks of every work item: per sequence (or segment) the
-// dq and dk walks of all heads, which take longer, then the dv walks.
+// dq and dk walks of all heads, which take longer, then the dv walks, those of
+// the heads from dv_whole on by half heads.
 template <typename E, int NW, bool DG>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_grad_kernel(const LinearGradArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int CB = 8 / NW;
-  const int H = p.dq.num_heads, H8 = (H + 7) / 8 * 8;
-  const int per = 3 * CB * H8;  // blocks of an item; b and b + 8 run on the same XCD
-  const int64_t item = blockIdx.x / per;
-  const int at = blockIdx.x % per, slot8 = at >> 3;
-  int part, h;
-  if (at < 2 * CB * H8) {
-    part = slot8 % (2 * CB);
-    h = slot8 / (2 * CB) * 8 + (at & 7);
-  } else {
-    part = slot8 % CB + 2 * CB;
-    h = (slot8 - 2 * CB * (H8 / 8)) / CB * 8 + (at & 7);
+  const GradGrid grid(p.dq.num_heads, CB, p.dv_whole);
+  const int H = p.dq.num_heads;
+  const int64_t item = blockIdx.x / grid.blocks;
+  int at = blockIdx.x % grid.blocks;  // b and b + 8 run on the same XCD
+  auto head = [&](int cbs, int& part) {
+    part = (at >> 3) % cbs;
+    return (at >> 3) / cbs * 8 + (at & 7);
+  };
+  int part;
+  if (at < grid.heavy) {
+    const int h = head(2 * CB, part);
+    if (h >= H) return;
+    if (part < CB) walk<E, NW, true, true, true, DG>(p.dk, smem, item * H + h, part);
+    else walk<E, NW, false, true, true, DG>(p.dq, smem, item * H + h, part - CB);
+    return;
   }
-  if (h >= H) return;
-  const int64_t u = item * H + h;
-  const int cb = part % CB;
-  if (part < CB) walk<E, NW, true, true, true, DG>(p.dk, smem, u, cb);
-  else if (part < 2 * CB) walk<E, NW, false, true, true, DG>(p.dq, smem, u, cb);
-  else walk<E, NW, true, false, true, false>(p.dv, smem, u, cb);
+  at -= grid.heavy;
+  if (at < grid.whole) {
+    const int h = head(CB, part);
+    if (h < p.dv_whole) walk<E, NW, true, false, true, false>(p.dv, smem, item * H + h, part);
+  } else if constexpr (NW == 8) {
+    at -= grid.whole;
+    const int h = p.dv_whole + head(2, part);
+    if (h < H && threadIdx.x < 64 * (4 + 4)) walk<E, 4, true, false, true, false>(p.dv, smem, item * H + h, part);
+  }
 }
 
 // Dynamic LDS above 64 KiB has to be asked for, once per device.
@@ -1148,11 +1156,11 @@ hipError_t launch_walk_e(const LinearWalkArgs& a, hipStream_t stream) {
 template <typename E, int NW, bool DG>
 hipError_t launch_grad_t(const LinearGradArgs& a, hipStream_t stream) {
   constexpr int LDS = std::max({WalkLayout<E, NW, DG, DG>::BYTES, WalkLayout<E, NW, DG, false>::BYTES,
-                                WalkLayout<E, NW, false, false>::BYTES});
+                                WalkLayout<E, NW, false, false>::BYTES, WalkLayout<E, 4, false, false>::BYTES});
   static std::atomic<bool> set[64];
   hipError_t e = allow_lds(linear_grad_kernel<E, NW, DG>, LDS, set);
   if (e != hipSuccess) return e;
-  const int64_t H = a.dq.num_heads, blocks = a.dq.units / H * ((H + 7) / 8 * 8) * 3 * (8 / NW);
+  const int64_t blocks = a.dq.units / a.dq.num_heads * GradGrid(a.dq.num_heads, 8 / NW, a.dv_whole).blocks;
   hipLaunchKernelGGL((linear_grad_kernel<E, NW, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
   return hipGetLastError();
 }
@@ -1168,7 +1176,7 @@ hipError_t launch_grad_e(const LinearGradArgs& a, hipStream_t stream) {
 //   D_t = <S, dS> at the stretch's end + sum over t' >= t of r_t' - c_t',
 // in fp64, from the stretch's end on, 1024 tokens a turn (four a thread).
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void linear_decay_grad_kernel(const LinearDecayGradArgs a) {
+__device__ __forceinline__ void decay_grad(const LinearDecayGradArgs& a) {
   constexpr size_t kState = (size_t)D * D;
   const int H = a.num_heads;
   const int h = (int)(blockIdx.x % H);
@@ -1289,21 +1297,31 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Gradients of shared query and key heads: the sum over the value heads that
-// share one, in order.  Four consecutive channels per thread.
+// What follows the gradients' walks, in one launch: the decays' gradient, and
+// the gradients of shared query and key heads, summed over the value heads that
+// share one, in order (four consecutive channels per thread).
 // ---------------------------------------------------------------------------
 template <typename E>
-__global__ __launch_bounds__(256) void linear_share_sum_kernel(const float* __restrict__ src, E* __restrict__ dst,
-                                                               const int32_t* cu, int num_seqs, int64_t total_tokens,
-                                                               int heads, int share) {
-  const int64_t rows = (cu ? clamp_cu(cu, num_seqs, total_tokens) : total_tokens) * heads;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void linear_finish_kernel(const LinearFinishArgs a) {
+  int64_t b = blockIdx.x;
+  if (b < a.decay_blocks) {
+    decay_grad(a.decay);
+    return;
+  }
+  b -= a.decay_blocks;
+  const bool of_dk = b >= a.share_blocks;
+  if (of_dk) b -= a.share_blocks;
+  const LinearDecayGradArgs& d = a.decay;
+  const int64_t T = d.cu ? clamp_cu(d.cu, d.num_seqs, d.total_tokens) : d.total_tokens;
+  const int64_t i = b * 256 + threadIdx.x;
   const int64_t row = i >> 5;
   const int ch = (int)(i & 31) * 4;
-  if (row >= rows) return;
+  if (row >= T * a.qk_heads) return;
+  const int share = d.num_heads / a.qk_heads;
+  const float* src = a.share + (of_dk ? (size_t)d.total_tokens * d.num_heads * D : 0);
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < share; ++j) s += *reinterpret_cast<const f32x4*>(src + (row * share + j) * D + ch);
-  store_row4(dst + row * D + ch, s);
+  store_row4(static_cast<E*>(of_dk ? a.dk : a.dq) + row * D + ch, s);
 }
 
 __global__ __launch_bounds__(64) void linear_decay_sum_kernel(const double* __restrict__ part, float* __restrict__ dst,
@@ -1326,9 +1344,14 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream) {
   return a.dq.bf16 ? launch_grad_e<__bf16>(a, stream) : launch_grad_e<float>(a, stream);
 }
 
-hipError_t launch_linear_decay_grad(const LinearDecayGradArgs& a, hipStream_t stream) {
-  const int64_t blocks = linear_slots(a.total_tokens, a.num_seqs, a.anchor) * a.num_heads;
-  hipLaunchKernelGGL(linear_decay_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t stream) {
+  const LinearDecayGradArgs& d = a.decay;
+  a.decay_blocks = a.decay_blocks ? linear_slots(d.total_tokens, d.num_seqs, d.anchor) * d.num_heads : 0;
+  a.share_blocks = a.share ? (d.total_tokens * a.qk_heads * 32 + 255) / 256 : 0;
+  const int64_t blocks = a.decay_blocks + 2 * a.share_blocks;
+  if (blocks == 0) return hipSuccess;
+  if (bf16) hipLaunchKernelGGL(linear_finish_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(linear_finish_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -1338,19 +1361,6 @@ hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(linear_scan_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL(linear_scan_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_share_sum(const float* src, void* dst, const LinearWalkArgs& a, hipStream_t stream) {
-  const int heads = a.x_heads, share = a.num_heads / heads;
-  const int64_t blocks = (a.total_tokens * heads * 32 + 255) / 256;
-  if (blocks == 0) return hipSuccess;
-  if (a.bf16)
-    hipLaunchKernelGGL(linear_share_sum_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, stream, src,
-                       static_cast<__bf16*>(dst), a.cu, a.num_seqs, a.total_tokens, heads, share);
-  else
-    hipLaunchKernelGGL(linear_share_sum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, stream, src,
-                       static_cast<float*>(dst), a.cu, a.num_seqs, a.total_tokens, heads, share);
   return hipGetLastError();
 }
 

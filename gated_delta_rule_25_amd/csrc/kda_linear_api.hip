@@ -86,6 +86,35 @@ void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num
   pl.slots = kda::linear_slots(total_tokens, num_seqs, pl.seg);
 }
 
+// One sequence, one walk each: of the heads' dv walks that start last, when
+// twice as many would find a free unit as well, half heads shorten the end.
+// The walks start in order (dq and dk of all heads, then dv), one to a unit; a
+// dv walk takes 2 where the others take 3 (2 without the decays' gradient), by
+// half heads 1.5 (96 heads x 8192 tokens on 256 units: 610, 400 and 300 us).
+int whole_dv_heads(int heads, bool decay_grad, int cus) {
+  const int kTimes = 64;                     // units that come free by time (in a ring)
+  int64_t free_at[kTimes] = {(int64_t)cus};
+  auto start = [&](int64_t& now, int64_t& walks, int time) {
+    while (free_at[now % kTimes] == 0) ++now;
+    const int64_t n = std::min(free_at[now % kTimes], walks);
+    free_at[now % kTimes] -= n;
+    free_at[(now + time) % kTimes] += n;
+    walks -= n;
+    return n;
+  };
+  int64_t now = 0, walks = 2 * (int64_t)heads;
+  while (walks > 0) start(now, walks, decay_grad ? 3 : 2);
+  const int64_t heavy_end = now + (decay_grad ? 3 : 2);
+  walks = heads;
+  while (walks > 0) {
+    while (free_at[now % kTimes] == 0) ++now;
+    const int64_t idle = free_at[now % kTimes];
+    const int64_t n = start(now, walks, 2);
+    if (walks == 0 && 2 * n <= idle && now + 2 > heavy_end) return heads - (int)n;
+  }
+  return heads;
+}
+
 bool plan_ok(const LinearPlan& pl, int num_heads) {
   return std::max(pl.slots, pl.anchored) * num_heads <= (int64_t)INT32_MAX / 4;
 }
@@ -379,6 +408,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   };
   kda::LinearGradArgs g;
   g.decay_grad = grad;
+  g.dv_whole = num_seqs == 1 && !pl.segmented && !pl.narrow
+                   ? whole_dv_heads(num_heads, grad, cu_count_for_current_device())
+                   : num_heads;
   g.dq = role(base, d_o, hv, v, hv, k, hq);
   g.dq.init = initial_state;
   g.dq.snap = fsnap;
@@ -407,34 +439,33 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
     if (segment_states(g.dv, d_final_state, stream) != hipSuccess) return KDA_ERR_HIP;
   }
   if (kda::launch_linear_grad(g, stream) != hipSuccess) return KDA_ERR_HIP;
-  if (grad && total_tokens > 0) {
-    kda::LinearDecayGradArgs d;
-    std::memset(&d, 0, sizeof(d));
-    d.s_anchors = s_anchors;
-    d.ds_anchors = ds_anchors;
-    d.r = change;
-    d.c = change + pl.blocks * rows;
-    d.blocks = pl.blocks;
-    d.has_d_final = d_final_state != nullptr;
-    d.d_log_decay = per_head ? nullptr : d_log_decay;
-    d.part = per_head ? reinterpret_cast<double*>(ws + pl.off_part) : nullptr;
-    d.cu = cu_seqlens;
-    d.num_seqs = num_seqs;
-    d.total_tokens = total_tokens;
-    d.num_heads = num_heads;
-    d.anchor = (int)pl.anchor;
-    if (kda::launch_linear_decay_grad(d, stream) != hipSuccess) return KDA_ERR_HIP;
-  }
+  kda::LinearFinishArgs f;
+  std::memset(&f, 0, sizeof(f));
+  f.decay.s_anchors = s_anchors;
+  f.decay.ds_anchors = ds_anchors;
+  f.decay.r = change;
+  f.decay.c = change + pl.blocks * rows;
+  f.decay.blocks = pl.blocks;
+  f.decay.has_d_final = d_final_state != nullptr;
+  f.decay.d_log_decay = per_head ? nullptr : d_log_decay;
+  f.decay.part = per_head ? reinterpret_cast<double*>(ws + pl.off_part) : nullptr;
+  f.decay.cu = cu_seqlens;
+  f.decay.num_seqs = num_seqs;
+  f.decay.total_tokens = total_tokens;
+  f.decay.num_heads = num_heads;
+  f.decay.anchor = (int)pl.anchor;
+  f.decay_blocks = grad && total_tokens > 0;
+  f.share = shared ? share : nullptr;
+  f.dq = dq;
+  f.dk = dk;
+  f.qk_heads = num_qk_heads;
+  if (kda::launch_linear_finish(f, base.bf16, stream) != hipSuccess) return KDA_ERR_HIP;
   if (grad && per_head) {
     // (no tokens: no stretch, and the sums are zero)
     const int64_t units = total_tokens > 0 ? (int64_t)anchored : 0;
     if (kda::launch_linear_decay_sum(reinterpret_cast<double*>(ws + pl.off_part), d_log_decay, units, num_heads,
                                      stream) != hipSuccess)
       return KDA_ERR_HIP;
-  }
-  if (shared) {
-    if (kda::launch_linear_share_sum(share, dq, g.dq, stream) != hipSuccess) return KDA_ERR_HIP;
-    if (kda::launch_linear_share_sum(share + rows * kD, dk, g.dk, stream) != hipSuccess) return KDA_ERR_HIP;
   }
   return KDA_OK;
 }

@@ -62,6 +62,18 @@ struct LinearWalkArgs {
 struct LinearGradArgs {
   LinearWalkArgs dq, dk, dv;
   bool decay_grad;
+  int dv_whole;            // heads whose dv walk is whole; half heads for the rest (whole heads elsewhere only)
+};
+
+// Blocks of a work item in the launch of the three walks, in multiples of 8
+// (XCDs): dq and dk, dv by whole heads (or the column blocks all take), dv by
+// half heads.
+struct GradGrid {
+  int heavy, whole, blocks;
+  __host__ __device__ GradGrid(int heads, int column_blocks, int dv_whole)
+      : heavy(2 * column_blocks * round8(heads)), whole(column_blocks * round8(dv_whole)),
+        blocks(heavy + whole + 2 * round8(heads - dv_whole)) {}
+  static __host__ __device__ int round8(int x) { return (x + 7) / 8 * 8; }
 };
 
 struct LinearDecayGradArgs {
@@ -78,6 +90,16 @@ struct LinearDecayGradArgs {
   int64_t total_tokens;
   int num_heads;
   int anchor;
+};
+
+struct LinearFinishArgs {
+  LinearDecayGradArgs decay;  // (its sizes and cu also hold for the sums over shared heads)
+  int64_t decay_blocks;       // nonzero: the decays' gradient is wanted
+  const float* share;         // [2][T, H, 128] fp32 gradients of the value heads' dq and dk, or null
+  void* dq;                   // [T, qk_heads, 128] in the I/O dtype
+  void* dk;
+  int qk_heads;
+  int64_t share_blocks;       // set by the launch
 };
 
 struct LinearScanArgs {
@@ -108,11 +130,8 @@ struct LinearDecodeArgs {
 
 hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream);
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream);
-hipError_t launch_linear_decay_grad(const LinearDecayGradArgs& a, hipStream_t stream);
+hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t stream);
 hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream);
-// dst[t][g] = sum over the `share` heads of group g of src[t][g share + i], fp32 to the I/O dtype.
-hipError_t launch_linear_share_sum(const float* src, void* dst, const LinearWalkArgs& a, hipStream_t stream);
-// dst[h] = sum over the work items u with u % num_heads = h of part[u], in order.
 hipError_t launch_linear_decay_sum(const double* part, float* dst, int64_t units, int num_heads, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearDecodeArgs& a, hipStream_t stream);
 // Checks the documented input ranges (log_decay <= 0 and not NaN; cu_seqlens)

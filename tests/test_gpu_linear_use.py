@@ -91,6 +91,14 @@ def test_one_sequence_of_many_heads(dtype):
     check_backward(d, lengths, dtype)
 
 
+@pytest.mark.parametrize("need_dg", [True, False])
+@pytest.mark.parametrize("h", [90, 128])
+def test_backward_whose_last_walks_take_half_heads(h, need_dg):
+    # (on 256 compute units: 76 heads' dv whole and 14 by halves, none whole)
+    lengths = [70]
+    check_backward(lt.make(lengths, h, h // 2, "bf16", "token", True, 49, DEV), lengths, "bf16", need_dg=need_dg)
+
+
 def test_segments_that_the_gradient_cuts_further():
     # 1088 tokens hold no stretch of 512 tokens or fewer but 64 x 17's own divisors
     lengths = [1500]
