@@ -93,7 +93,7 @@ def _load():
     lib.kda_linear_chunk_fwd.restype = i32
     lib.kda_linear_chunk_fwd.argtypes = [vp] * 6 + [i32, i64] + [i32] * 7 + [vp, vp, vp, sz, vp]
     lib.kda_linear_chunk_bwd_workspace_bytes.restype = sz
-    lib.kda_linear_chunk_bwd_workspace_bytes.argtypes = [i32, i64] + [i32] * 8
+    lib.kda_linear_chunk_bwd_workspace_bytes.argtypes = [i32, i64] + [i32] * 9
     lib.kda_linear_chunk_bwd.restype = i32
     lib.kda_linear_chunk_bwd.argtypes = [vp] * 8 + [i32, i64] + [i32] * 7 + [vp] * 6 + [sz, vp]
     lib.kda_linear_decode_step.restype = i32

@@ -31,6 +31,7 @@
 // then writes it, so the rows change in place with no copy of the states and
 // no barrier, and rows that stay are not touched.  Bound by HBM (64 groups of 4
 // beams, 96 heads of states and histories: 370 us, 5.7 TB/s of what moves).
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
 template <typename T, int KMAX>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(const BeamReorderArgs a) {
   const int64_t blk = blockIdx.x % a.blocks;
-  const int64_t g = blockIdx.x / a.blocks;
+  const int64_t g = a.group0 + blockIdx.x / a.blocks;
   const int K = a.beams;
   int s = 0;
   while (s + 1 < a.count && blk >= a.block0[s + 1]) ++s;
@@ -511,13 +512,17 @@ static hipError_t launch_reorder_t(BeamReorderArgs a, hipStream_t stream) {
     a.block0[s] = a.blocks;
     a.blocks += (a.row_units[s] + 255) / 256;
   }
-  const int64_t grid = a.blocks * a.groups;
-  if (grid == 0) return hipSuccess;
-  const dim3 g((unsigned)grid), b(256);
-  if (a.beams <= 4) hipLaunchKernelGGL((beam_reorder_kernel<T, 4>), g, b, 0, stream, a);
-  else if (a.beams <= 8) hipLaunchKernelGGL((beam_reorder_kernel<T, 8>), g, b, 0, stream, a);
-  else hipLaunchKernelGGL((beam_reorder_kernel<T, 16>), g, b, 0, stream, a);
-  return hipGetLastError();
+  if (a.blocks == 0) return hipSuccess;
+  const int64_t most = UINT32_MAX / 256 / a.blocks;  // groups of a launch (below 2^32 threads)
+  for (a.group0 = 0; a.group0 < a.groups; a.group0 += most) {
+    const dim3 g((unsigned)(std::min(a.groups - a.group0, most) * a.blocks)), b(256);
+    if (a.beams <= 4) hipLaunchKernelGGL((beam_reorder_kernel<T, 4>), g, b, 0, stream, a);
+    else if (a.beams <= 8) hipLaunchKernelGGL((beam_reorder_kernel<T, 8>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((beam_reorder_kernel<T, 16>), g, b, 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_beam_reorder(const BeamReorderArgs& a, int unit, hipStream_t stream) {

@@ -34,7 +34,7 @@ SelectLayout select_layout(int groups, int beams, const kda::BeamPlan& pl) {
 }
 
 bool select_grid_ok(int groups, int beams, const kda::BeamPlan& pl) {
-  return (int64_t)groups * beams * pl.slices <= (int64_t)INT32_MAX;
+  return (int64_t)groups * beams * pl.slices * kda::kBeamThreads <= (int64_t)UINT32_MAX;  // threads of a launch
 }
 
 }  // namespace
@@ -122,7 +122,7 @@ kda_status kda_beam_reorder(void* const* states, const int64_t* row_bytes, int n
   for (int i = 0; i <= num_states; ++i)
     for (int j = i + 1; j <= num_states; ++j)
       if (overlap(used[i], used[j])) return KDA_ERR_INVALID_ARG;
-  if (blocks > (int64_t)INT32_MAX / groups) return KDA_ERR_INVALID_ARG;
+  if (blocks * 256 > (int64_t)UINT32_MAX) return KDA_ERR_INVALID_ARG;  // threads of a launch, for one group
   for (int u : {16, 4, 1}) {
     kda::BeamReorderArgs a;
     std::memset(&a, 0, sizeof(a));

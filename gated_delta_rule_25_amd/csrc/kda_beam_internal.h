@@ -68,6 +68,7 @@ struct BeamReorderArgs {
   const int32_t* parents;             // [groups, beams]
   int groups;
   int beams;
+  int64_t group0;                     // first group of the launch (set by it)
 };
 
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t stream);

@@ -85,6 +85,9 @@ __device__ __forceinline__ Segment find_segment(const int32_t* cu, int N, int64_
 __device__ __forceinline__ int64_t slot_of(int n, int64_t bos, int seg, int64_t j) {
   return bos / seg + 2 * (int64_t)n + j;
 }
+__device__ __forceinline__ int64_t boundary_of(int n, int64_t bos, int anchor, bool ends, int64_t j) {
+  return bos / anchor + (ends ? n : 0) + j - 1;
+}
 
 // Sequence of rank r when the sequences are ordered longest first (ties by
 // index), so that the longest walks start first.  Every thread of the
@@ -811,10 +814,14 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     }
   };
   constexpr size_t kState = (size_t)D * D;
-  // what the decays' gradient needs of the state: S entering stretch j of
-  // `anchor` tokens (dq walk), dS behind it (dk walk)
+  // what the decays' gradient needs of the state (S in the dq walk, dS in the
+  // dk walk) at boundary j of the sequence's stretches of `anchor` tokens
+  const int64_t stretches = DG ? (eos - bos + p.anchor - 1) / p.anchor : 0;
   auto leave_state = [&](int64_t j, const f32x4 (&s)[8]) {
-    store_state(p.anchors + ((size_t)slot_of(n, bos, p.anchor, j) * H + h) * kState, s);
+    if (j == 0 || (j == stretches && !p.end_state)) return;
+    const int64_t at = p.anchors == p.snap ? slot_of(n, bos, p.anchor, j)
+                                           : boundary_of(n, bos, p.anchor, p.end_state, j);
+    store_state(p.anchors + ((size_t)at * H + h) * kState, s);
   };
   f32x4 accS[8];
   {
@@ -878,7 +885,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   read_q(base, 0);
   read_q(base, 1);
   int boundary = 0;  // chunks to the next one
-  int64_t stretch_at = DG ? (REV ? (te - bos + p.anchor - 1) / p.anchor - 1 : (tb - bos) / p.anchor) : 0;
+  int64_t stretch_at = DG ? (REV ? (te - bos + p.anchor - 1) / p.anchor : (tb - bos) / p.anchor) : 0;
   for (int ci = 0; ci < nch; ++ci) {
     const int64_t t0 = tb + (int64_t)chunk_of(ci) * C;
     const int nv = (int)min((int64_t)C, te - t0);
@@ -1077,7 +1084,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   if (OUT) {
     if (p.fin && (REV ? first : last)) store_state(p.fin + nh * kState, accS);
     if constexpr (DG && !REV)
-      if (last && nch > 0) leave_state((eos - bos + p.anchor - 1) / p.anchor, accS);
+      if (last && nch > 0) leave_state(stretches, accS);
   } else {
     store_state(p.snap + ((size_t)slot * H + h) * kState, accS);
   }
@@ -1089,7 +1096,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const Linear
   // Blocks b and b + 8 run on the same XCD: what a head's column blocks both
   // read comes from its L2 the second time.
   constexpr int CB = 8 / NW;
-  const int64_t slot8 = blockIdx.x >> 3, u = slot8 / CB * 8 + (blockIdx.x & 7);
+  const int64_t slot8 = blockIdx.x >> 3, u = p.unit0 + slot8 / CB * 8 + (blockIdx.x & 7);
   const int cb = (int)(slot8 % CB);
   if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, cb);
 }
@@ -1103,7 +1110,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_grad_kernel(const Linear
   constexpr int CB = 8 / NW;
   const GradGrid grid(p.dq.num_heads, CB, p.dv_whole);
   const int H = p.dq.num_heads;
-  const int64_t item = blockIdx.x / grid.blocks;
+  const int64_t item = p.item0 + blockIdx.x / grid.blocks;
   int at = blockIdx.x % grid.blocks;  // b and b + 8 run on the same XCD
   auto head = [&](int cbs, int& part) {
     part = (at >> 3) % cbs;
@@ -1128,6 +1135,9 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_grad_kernel(const Linear
   }
 }
 
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = 0xffffffffll;
+
 // Dynamic LDS above 64 KiB has to be asked for, once per device.
 template <typename K>
 hipError_t allow_lds(K kernel, int bytes, std::atomic<bool> (&set)[64]) {
@@ -1147,9 +1157,17 @@ hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
   static std::atomic<bool> set[64];
   hipError_t e = allow_lds(linear_walk_kernel<E, NW, REV, OUT>, LDS, set);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (a.units + 7) / 8 * 8 * (8 / NW);
-  hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, OUT>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
-  return hipGetLastError();
+  constexpr int CB = 8 / NW, THREADS = 64 * (NW + 4);
+  constexpr int64_t MOST = kMaxThreads / THREADS / (8 * CB) * 8;  // units of a launch
+  LinearWalkArgs part = a;
+  for (part.unit0 = 0; part.unit0 < a.units; part.unit0 += MOST) {
+    part.units = std::min(a.units, part.unit0 + MOST);
+    const int64_t blocks = (part.units - part.unit0 + 7) / 8 * 8 * CB;
+    hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, OUT>), dim3((unsigned)blocks), dim3(THREADS), LDS, stream, part);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename E>
@@ -1165,9 +1183,18 @@ hipError_t launch_grad_t(const LinearGradArgs& a, hipStream_t stream) {
   static std::atomic<bool> set[64];
   hipError_t e = allow_lds(linear_grad_kernel<E, NW, DG>, LDS, set);
   if (e != hipSuccess) return e;
-  const int64_t blocks = a.dq.units / a.dq.num_heads * GradGrid(a.dq.num_heads, 8 / NW, a.dv_whole).blocks;
-  hipLaunchKernelGGL((linear_grad_kernel<E, NW, DG>), dim3((unsigned)blocks), dim3(64 * (NW + 4)), LDS, stream, a);
-  return hipGetLastError();
+  constexpr int THREADS = 64 * (NW + 4);
+  const int64_t items = a.dq.units / a.dq.num_heads;
+  const int per = GradGrid(a.dq.num_heads, 8 / NW, a.dv_whole).blocks;
+  const int64_t most = kMaxThreads / THREADS / per;  // items of a launch (65535 heads: 14)
+  LinearGradArgs part = a;
+  for (part.item0 = 0; part.item0 < items; part.item0 += most) {
+    const int64_t blocks = std::min(items - part.item0, most) * per;
+    hipLaunchKernelGGL((linear_grad_kernel<E, NW, DG>), dim3((unsigned)blocks), dim3(THREADS), LDS, stream, part);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename E>
@@ -1205,8 +1232,10 @@ __device__ __forceinline__ void decay_grad(const LinearDecayGradArgs& a) {
     const int64_t tb = s.bos + (int64_t)s.j * a.anchor, te = min(s.eos, tb + (int64_t)a.anchor);
     double flow = 0.0;
     if (s.j + 1 < s.count || a.has_d_final) {
-      const float* S = a.s_anchors + ((size_t)(slot + 1) * H + h) * kState;  // entering the next stretch
-      const float* M = a.ds_anchors + ((size_t)slot * H + h) * kState;
+      const int64_t at = boundary_of(s.n, s.bos, a.anchor, a.has_d_final, s.j + 1);
+      // (segments: what enters the next one, and what enters this one backwards)
+      const float* S = a.s_anchors + ((size_t)(a.own ? at : slot + 1) * H + h) * kState;
+      const float* M = a.ds_anchors + ((size_t)(a.own ? at : slot) * H + h) * kState;
       double d = 0.0;
       for (int i = 0; i < 16; ++i) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(S + i * 1024 + 4 * t);
@@ -1275,7 +1304,7 @@ template <bool REV>
 __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a) {
   constexpr size_t kState = (size_t)D * D;
   const int H = a.num_heads;
-  const int64_t nh = blockIdx.x >> 4;
+  const int64_t nh = a.unit0 + (blockIdx.x >> 4);
   const int at = ((int)(blockIdx.x & 15) * 256 + threadIdx.x) * 4;
   const int n = (int)(nh / H), h = (int)(nh % H);
   int64_t bos, eos;
@@ -1320,15 +1349,17 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(const LinearFinishAr
   if (of_dk) b -= a.share_blocks;
   const LinearDecayGradArgs& d = a.decay;
   const int64_t T = d.cu ? clamp_cu(d.cu, d.num_seqs, d.total_tokens) : d.total_tokens;
-  const int64_t i = b * 256 + threadIdx.x;
-  const int64_t row = i >> 5;
-  const int ch = (int)(i & 31) * 4;
-  if (row >= T * a.qk_heads) return;
   const int share = d.num_heads / a.qk_heads;
   const float* src = a.share + (of_dk ? (size_t)d.total_tokens * d.num_heads * D : 0);
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < share; ++j) s += *reinterpret_cast<const f32x4*>(src + (row * share + j) * D + ch);
-  store_row4(static_cast<E*>(of_dk ? a.dk : a.dq) + row * D + ch, s);
+  E* dst = static_cast<E*>(of_dk ? a.dk : a.dq);
+  const int64_t rows = T * a.qk_heads;
+  for (int64_t i = b * 256 + threadIdx.x; (i >> 5) < rows; i += a.share_blocks * 256) {
+    const int64_t row = i >> 5;
+    const int ch = (int)(i & 31) * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < share; ++j) s += *reinterpret_cast<const f32x4*>(src + (row * share + j) * D + ch);
+    store_row4(dst + row * D + ch, s);
+  }
 }
 
 __global__ __launch_bounds__(64) void linear_decay_sum_kernel(const double* __restrict__ part, float* __restrict__ dst,
@@ -1354,7 +1385,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream) {
 hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t stream) {
   const LinearDecayGradArgs& d = a.decay;
   a.decay_blocks = a.decay_blocks ? linear_slots(d.total_tokens, d.num_seqs, d.anchor) * d.num_heads : 0;
-  a.share_blocks = a.share ? (d.total_tokens * a.qk_heads * 32 + 255) / 256 : 0;
+  a.share_blocks = a.share ? std::min((d.total_tokens * a.qk_heads * 32 + 255) / 256, (int64_t)1 << 20) : 0;
   const int64_t blocks = a.decay_blocks + 2 * a.share_blocks;
   if (blocks == 0) return hipSuccess;
   if (bf16) hipLaunchKernelGGL(linear_finish_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
@@ -1363,12 +1394,17 @@ hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t strea
 }
 
 hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream) {
-  const int64_t blocks = (int64_t)a.num_seqs * a.num_heads * 16;
-  if (a.reverse)
-    hipLaunchKernelGGL(linear_scan_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(linear_scan_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  const int64_t units = (int64_t)a.num_seqs * a.num_heads;
+  constexpr int64_t MOST = kMaxThreads / 256 / 16;
+  LinearScanArgs part = a;
+  for (part.unit0 = 0; part.unit0 < units; part.unit0 += MOST) {
+    const dim3 grid((unsigned)(std::min(units - part.unit0, MOST) * 16));
+    if (a.reverse) hipLaunchKernelGGL(linear_scan_kernel<true>, grid, dim3(256), 0, stream, part);
+    else hipLaunchKernelGGL(linear_scan_kernel<false>, grid, dim3(256), 0, stream, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_linear_decay_sum(const double* part, float* dst, int64_t units, int num_heads, hipStream_t stream) {

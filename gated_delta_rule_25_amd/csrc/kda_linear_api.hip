@@ -39,6 +39,7 @@ struct LinearPlan {
   int64_t seg = kAnchorTokens;
   int64_t slots = 0;     // segments, empty ones included
   int64_t anchored = 0;  // stretches of the decays' gradient, likewise
+  int64_t boundaries = 0;  // states between them
   int64_t anchor = kAnchorTokens;
   bool own_anchors = false;  // boundary states apart from the segments'
   int blocks = 1;            // column blocks of a head
@@ -116,7 +117,9 @@ int whole_dv_heads(int heads, bool decay_grad, int cus) {
 }
 
 bool plan_ok(const LinearPlan& pl, int num_heads) {
-  return std::max(pl.slots, pl.anchored) * num_heads <= (int64_t)INT32_MAX / 4;
+  // (one workgroup of 256 threads per stretch in a launch of below 2^32 threads,
+  // beside 2^21 others)
+  return pl.slots * num_heads <= (int64_t)INT32_MAX / 4 && pl.anchored * num_heads <= (int64_t)14 << 20;
 }
 
 LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus) {
@@ -140,7 +143,7 @@ LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
 // c_t [column blocks][H][T]; the stretches' sums of a constant decay's
 // gradient; the fp32 gradients [T, H, 128] that shared heads are summed from.
 LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads, int segment_tokens,
-                         bool decay_grad, bool decay_per_head, int cus) {
+                         bool decay_grad, bool decay_per_head, bool d_final, int cus) {
   LinearPlan pl;
   choose_segments(pl, num_seqs, total_tokens, num_heads, segment_tokens, cus, true);
   const size_t units = (size_t)pl.slots * num_heads;
@@ -156,6 +159,7 @@ LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
   pl.own_anchors = decay_grad && !(pl.segmented && pl.anchor == pl.seg);
   pl.anchored = decay_grad ? kda::linear_slots(total_tokens, num_seqs, pl.anchor) : 0;
   const size_t anchored = (size_t)pl.anchored * num_heads;
+  if (pl.own_anchors) pl.boundaries = kda::linear_boundaries(total_tokens, num_seqs, pl.anchor, d_final);
   pl.blocks = pl.narrow ? 2 : 1;
   size_t off = 0;
   pl.off_fsnap = off;
@@ -163,7 +167,7 @@ LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
   pl.off_rsnap = off;
   if (pl.segmented) off += units * kStateBytes;
   pl.off_anchor = off;
-  if (pl.own_anchors) off += 2 * anchored * kStateBytes;
+  off += 2 * (size_t)pl.boundaries * num_heads * kStateBytes;
   pl.off_decay = off;
   if (pl.segmented) off += align256(units * sizeof(float));
   pl.off_change = off;
@@ -309,13 +313,14 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
 }
 
 size_t kda_linear_chunk_bwd_workspace_bytes(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads,
-                                            int decay_per_head, int need_d_log_decay, int d_k, int d_v,
-                                            kda_dtype dtype, int segment_tokens) {
+                                            int decay_per_head, int need_d_log_decay, int with_d_final_state, int d_k,
+                                            int d_v, kda_dtype dtype, int segment_tokens) {
   if (!linear_sizes_ok(num_seqs, total_tokens, num_heads, num_qk_heads) || d_k != kD || d_v != kD || !dtype_ok(dtype))
     return 0;
   if (segment_tokens > 0 && segment_tokens % 64 != 0) return 0;
   const LinearPlan pl = make_bwd_plan(num_seqs, total_tokens, num_heads, num_qk_heads, segment_tokens,
-                                      need_d_log_decay != 0, decay_per_head != 0, cu_count_for_current_device());
+                                      need_d_log_decay != 0, decay_per_head != 0, with_d_final_state != 0,
+                                      cu_count_for_current_device());
   return plan_ok(pl, num_heads) ? pl.bytes : 0;
 }
 
@@ -338,7 +343,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   }
   const bool grad = d_log_decay != nullptr, per_head = decay_per_head != 0;
   const LinearPlan pl = make_bwd_plan(num_seqs, total_tokens, num_heads, num_qk_heads, segment_tokens, grad, per_head,
-                                      cu_count_for_current_device());
+                                      d_final_state != nullptr, cu_count_for_current_device());
   if (!plan_ok(pl, num_heads)) return KDA_ERR_INVALID_ARG;
   if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return KDA_ERR_WORKSPACE;
 
@@ -376,7 +381,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   const size_t anchored = (size_t)pl.anchored * num_heads;
   float* anchors = reinterpret_cast<float*>(ws + pl.off_anchor);
   float* s_anchors = pl.own_anchors ? anchors : fsnap;
-  float* ds_anchors = pl.own_anchors ? anchors + anchored * kD * kD : rsnap;
+  float* ds_anchors = pl.own_anchors ? anchors + (size_t)pl.boundaries * num_heads * kD * kD : rsnap;
   float* change = reinterpret_cast<float*>(ws + pl.off_change);
 
   kda::LinearWalkArgs base;
@@ -390,6 +395,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   base.bf16 = dtype == KDA_DTYPE_BF16;
   base.seg = (int)pl.seg;
   base.anchor = (int)pl.anchor;
+  base.end_state = d_final_state != nullptr;
   base.segmented = pl.segmented;
   base.narrow = pl.narrow;
   base.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
@@ -443,6 +449,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   std::memset(&f, 0, sizeof(f));
   f.decay.s_anchors = s_anchors;
   f.decay.ds_anchors = ds_anchors;
+  f.decay.own = pl.own_anchors;
   f.decay.r = change;
   f.decay.c = change + pl.blocks * rows;
   f.decay.blocks = pl.blocks;
@@ -482,6 +489,7 @@ kda_status kda_linear_decode_step(float* state, const void* q, const void* k, co
       !aligned(log_decay, 4))
     return KDA_ERR_INVALID_ARG;
   const size_t units = (size_t)num_seqs * num_heads;
+  if (units * 256 > UINT32_MAX) return KDA_ERR_INVALID_ARG;  // a workgroup each, below 2^32 threads
   const size_t qk = (size_t)num_seqs * num_qk_heads * kD * es;
   const int64_t decays = decay_per_head ? num_heads : (int64_t)units;
   const Range ins[] = {range_of(q, qk), range_of(k, qk), range_of(v, units * kD * es),

@@ -18,6 +18,15 @@ constexpr int64_t linear_slots(int64_t total_tokens, int num_seqs, int64_t seg) 
   return total_tokens / seg + 2 * (int64_t)num_seqs;
 }
 
+// Boundaries between a sequence's stretches of `anchor` tokens, and its end if
+// `ends`: boundary j = 1 .. of sequence n has the index
+//   cu[n] / anchor + j - 1 (+ n with the ends),
+// again without two that meet, as a sequence has at most (L - 1) / anchor of
+// the former: nothing for sequences of one stretch.
+constexpr int64_t linear_boundaries(int64_t total_tokens, int num_seqs, int64_t anchor, bool ends) {
+  return total_tokens / anchor + (ends ? num_seqs : 0);
+}
+
 // One walk of a state over the chunks of a sequence or of a segment.  The
 // recurrence and its three gradients are the same walk with the tensors in
 // other roles:
@@ -41,6 +50,7 @@ struct LinearWalkArgs {
   int seg;                 // tokens per segment
   bool segmented;          // work items are (segment, head), else (sequence, head)
   int64_t units;           // work items
+  int64_t unit0;           // first item of the launch (set by it)
   bool reverse;            // backwards in time
   bool write_o;            // false: only each segment's own contribution to the state
   bool narrow;             // 64 value columns per workgroup instead of 128
@@ -52,15 +62,17 @@ struct LinearWalkArgs {
   bool o_f32;
   // gradient of the decays
   int anchor;              // tokens between the boundaries at which it is taken from the states (a multiple of 64)
-  float* anchors;          // [slots by `anchor`][H][128,128]: dq walk: S entering every stretch, and behind the last
-                           // token; dk walk: dS behind every stretch (written; `snap` itself when segments are of
-                           // that length and the scan has left them there)
+  bool end_state;          // a sequence's end is such a boundary too (dS there is given)
+  float* anchors;          // [linear_boundaries][H][128,128] S (dq walk) or dS (dk walk) at the boundaries (written); or
+                           // `snap` itself when segments are of that length: the scan has left there what enters
+                           // them, and the dq walk adds S behind the last token
   float* change;           // [column blocks][H][T]: r_t (dq walk) or c_t (dk walk) by the block's columns (written)
 };
 
 // The three walks of the backward pass.
 struct LinearGradArgs {
   LinearWalkArgs dq, dk, dv;
+  int64_t item0;           // first sequence (or segment) of the launch (set by it)
   bool decay_grad;
   int dv_whole;            // heads whose dv walk is whole; half heads for the rest (whole heads elsewhere only)
 };
@@ -77,8 +89,9 @@ struct GradGrid {
 };
 
 struct LinearDecayGradArgs {
-  const float* s_anchors;
+  const float* s_anchors;  // as LinearWalkArgs::anchors
   const float* ds_anchors;
+  bool own;                // by boundaries (not by segments)
   const float* r;          // [blocks][H][T]
   const float* c;
   int blocks;
@@ -103,6 +116,7 @@ struct LinearFinishArgs {
 };
 
 struct LinearScanArgs {
+  int64_t unit0;           // first (sequence, head) of the launch (set by it)
   float* snap;             // contributions in, incoming states out
   const float* seg_decay;
   const float* init;       // as above

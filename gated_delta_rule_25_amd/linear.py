@@ -140,12 +140,12 @@ def linear_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
 def linear_chunk_bwd_workspace_bytes(num_seqs: int, total_tokens: int, num_heads: int,
                                      dtype: torch.dtype = torch.bfloat16, *, num_qk_heads: Optional[int] = None,
                                      decay_per_head: bool = False, need_d_log_decay: bool = True,
-                                     segment_tokens: int = 0) -> int:
+                                     with_d_final_state: bool = True, segment_tokens: int = 0) -> int:
     """Workspace bytes of linear_chunk_bwd on the current device."""
     return int(_load().kda_linear_chunk_bwd_workspace_bytes(num_seqs, total_tokens, num_heads,
                                                             num_qk_heads or num_heads, int(decay_per_head),
-                                                            int(need_d_log_decay), D, D, _DTYPES[dtype],
-                                                            segment_tokens))
+                                                            int(need_d_log_decay), int(with_d_final_state), D, D,
+                                                            _DTYPES[dtype], segment_tokens))
 
 
 def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, d_o: torch.Tensor,
@@ -174,8 +174,9 @@ def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     dg = torch.empty_like(log_decay) if need_d_log_decay else None
     ds = torch.empty((n, h, D, D), dtype=torch.float32, device=dev) if need_d_initial_state else None
     with _on(dev):
-        need = int(lib.kda_linear_chunk_bwd_workspace_bytes(n, t, h, hq, per_head, int(need_d_log_decay), D, D,
-                                                            _DTYPES[dt], segment_tokens))
+        need = int(lib.kda_linear_chunk_bwd_workspace_bytes(n, t, h, hq, per_head, int(need_d_log_decay),
+                                                            int(d_final_state is not None), D, D, _DTYPES[dt],
+                                                            segment_tokens))
         workspace, ws_bytes = _workspace(workspace, need, dev)
         rc = lib.kda_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
                                       _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state), n, t, h, hq, per_head, D, D,

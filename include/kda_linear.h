@@ -75,10 +75,14 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
                                 int d_v, kda_dtype dtype, int segment_tokens, void* o, float* final_state,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of device workspace kda_linear_chunk_bwd needs (0 as above). */
+/*
+ * Bytes of device workspace kda_linear_chunk_bwd needs (0 as above).
+ * need_d_log_decay and with_d_final_state: whether the call is given
+ * d_log_decay and d_final_state.
+ */
 size_t kda_linear_chunk_bwd_workspace_bytes(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads,
-                                            int decay_per_head, int need_d_log_decay, int d_k, int d_v,
-                                            kda_dtype dtype, int segment_tokens);
+                                            int decay_per_head, int need_d_log_decay, int with_d_final_state, int d_k,
+                                            int d_v, kda_dtype dtype, int segment_tokens);
 
 /*
  * Gradients of  L = sum_t <d_o_t, o_t> + <d_final_state, S_T>.

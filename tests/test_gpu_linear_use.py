@@ -107,6 +107,28 @@ def test_segments_that_the_gradient_cuts_further():
     check_backward(lt.make(lengths, 1, 1, "bf16", "token", True, 44, DEV), lengths, "bf16", segment_tokens=1088)
 
 
+def test_more_work_items_than_one_launch_takes():
+    """20000 sequences of one token x 96 heads: each is its own pair, so
+    o = (q . k) v and dq = (v . d_o) k, dk = (v . d_o) q, dv = (q . k) d_o."""
+    n, h = 20000, 96
+    g = torch.Generator(device=DEV).manual_seed(51)
+    q, k, v, d_o = (torch.randn(n, h, 128, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(4))
+    la = torch.full((h,), -0.5, device=DEV)
+    cu = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    o, _ = kda.linear_chunk_fwd(q, k, v, la, None, cu, output_final_state=False)
+    dq, dk, dv, dg, _ = kda.linear_chunk_bwd(q, k, v, la, d_o, None, cu, need_d_initial_state=False)
+    torch.cuda.synchronize()
+    for at in (0, 1, n // 2, n - 70, n - 1):
+        s = slice(at, at + 70)
+        x = [t[s].cpu().double() for t in (q, k, v, d_o)]
+        qk, vo = (x[0] * x[1]).sum(-1, keepdim=True), (x[2] * x[3]).sum(-1, keepdim=True)
+        mqk, mvo = (x[0] * x[1]).abs().sum(-1, keepdim=True), (x[2] * x[3]).abs().sum(-1, keepdim=True)
+        for got, want, mag in ((o, qk * x[2], mqk * x[2].abs()), (dq, vo * x[1], mvo * x[1].abs()),
+                               (dk, vo * x[0], mvo * x[0].abs()), (dv, qk * x[3], mqk * x[3].abs())):
+            assert lt.excess(got[s], want, lt.bf16_bound(mag)) <= 1, at
+    assert torch.equal(dg, torch.zeros_like(dg))  # a token's own pair does not pass a decay
+
+
 def test_no_tokens():
     d = lt.make([0, 0], 2, 1, "bf16", "head", True, 45, DEV)
     o, fin = fwd(d)
@@ -131,7 +153,7 @@ def test_backward_leaves_rows_behind_the_last_sequence(hq, seg):
     outs = [torch.full_like(dd["q"], 7.0), torch.full_like(dd["q"], 7.0), torch.full_like(dd["v"], 7.0),
             torch.full((T, 4), 7.0, device=DEV), torch.empty_like(d["initial_state"])]
     lib = kda._load()
-    need = int(lib.kda_linear_chunk_bwd_workspace_bytes(2, T, 4, hq, 0, 1, 128, 128, 1, seg))
+    need = int(lib.kda_linear_chunk_bwd_workspace_bytes(2, T, 4, hq, 0, 1, 1, 128, 128, 1, seg))
     ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device=DEV)  # NaN wherever it is read unwritten
     P = kda._ptr
     rc = lib.kda_linear_chunk_bwd(P(dd["q"]), P(dd["k"]), P(dd["v"]), P(dd["log_decay"]), P(d["initial_state"]),

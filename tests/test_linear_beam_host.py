@@ -128,12 +128,16 @@ def test_chunk_workspaces(lib):
     assert f(1, 1000, 4, 2, 128, 128, 9, 64) == 0
     assert f(1, 1 << 31, 4, 2, 128, 128, BF16, 64) == 0
     # backward without the decays' gradient: the states of both directions, decays, and the shared heads' fp32 sums
-    assert b(1, 1000, 4, 4, 0, 0, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512
-    assert b(1, 1000, 4, 2, 0, 0, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512 + 2 * 1000 * 4 * 128 * 4
-    assert b(1, 1000, 4, 4, 0, 0, 128, 128, BF16, -1) == 0
-    assert b(1, 1000, 4, 4, 0, 1, 128, 128, BF16, -1) > 0
+    assert b(1, 1000, 4, 4, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512
+    assert b(1, 1000, 4, 2, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512 + 2 * 1000 * 4 * 128 * 4
+    assert b(1, 1000, 4, 4, 0, 0, 1, 128, 128, BF16, -1) == 0
+    # with it, r and c per token, and one state of each direction per boundary: short sequences have none but
+    # their ends, and those only where a gradient arrives there (r and c of two halves of a head with few chains)
+    assert b(1, 1000, 4, 4, 0, 1, 0, 128, 128, BF16, -1) == 2 * 2 * 1000 * 4 * 4
+    assert b(1, 1000, 4, 4, 0, 1, 1, 128, 128, BF16, -1) == 2 * 2 * 1000 * 4 * 4 + 2 * 4 * state
+    assert b(500, 1000, 96, 96, 0, 1, 0, 128, 128, BF16, 0) == 2 * 1000 * 96 * 4
     # a segment length with a large prime factor is cut at every 64 tokens
-    assert b(1, 200000, 1, 1, 0, 1, 128, 128, BF16, 64 * 1021) > 2 * 3125 * state
+    assert b(1, 200000, 1, 1, 0, 1, 0, 128, 128, BF16, 64 * 1021) > 2 * 3125 * state
 
 
 def decode(lib, **kw):
@@ -146,7 +150,7 @@ def decode(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dk=64), UNSUPPORTED), (dict(dv=64), UNSUPPORTED), (dict(dt=5), UNSUPPORTED),
     (dict(N=0), INVALID), (dict(H=0), INVALID), (dict(Hq=3), INVALID), (dict(H=70000, Hq=1), INVALID),
-    (dict(S=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(N=1 << 23), INVALID), (dict(S=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(la=None), INVALID), (dict(o=None), INVALID), (dict(S=p(0, 8)), INVALID),
     (dict(o=p(0)), INVALID), (dict(o=p(1)), INVALID), (dict(o=p(4)), INVALID), (dict(q=p(0, 256)), INVALID),
 ])
@@ -164,7 +168,7 @@ def select(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), INVALID), (dict(K=0), INVALID), (dict(V=0), INVALID), (dict(K=17), UNSUPPORTED),
-    (dict(dt=9), UNSUPPORTED), (dict(B=1 << 30, K=16), INVALID),
+    (dict(dt=9), UNSUPPORTED), (dict(B=1 << 30, K=16), INVALID), (dict(B=1 << 21, K=16, V=8), INVALID),
     (dict(x=None), INVALID), (dict(s=None), INVALID), (dict(os=None), INVALID), (dict(ot=None), INVALID),
     (dict(op=None), INVALID), (dict(f=p(7)), INVALID), (dict(of=p(7)), INVALID),
     (dict(f=p(7), of=p(9), end=-1), INVALID), (dict(f=p(7), of=p(9), end=1000), INVALID),
@@ -202,6 +206,7 @@ def test_reorder_refusals(lib):
     assert reorder(lib, [p(0), None], [64, 64]) == INVALID
     assert reorder(lib, s, [64, -1]) == INVALID
     assert reorder(lib, s, [64, 1 << 62]) == INVALID
+    assert reorder(lib, [p(0)], [(1 << 32) + 1], B=1) == INVALID    # a row of more units than a launch has threads
     assert reorder(lib, [p(0), p(0)], [64, 64]) == INVALID          # the same tensor twice
     assert reorder(lib, [p(0), p(0, 256)], [64, 64]) == INVALID     # two that overlap
     assert reorder(lib, [p(0), p(9)], [64, 64]) == INVALID          # parents among the states
