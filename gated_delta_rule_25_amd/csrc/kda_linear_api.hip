@@ -152,9 +152,7 @@ LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
   if (pl.segmented) {
     // a segment's end is a boundary as well: the longest stretch of whole
     // 64-token chunks that divides it
-    int64_t parts = (pl.seg + pl.anchor - 1) / pl.anchor;
-    while (pl.seg % (64 * parts) != 0) ++parts;  // ends at seg / 64
-    pl.anchor = pl.seg / parts;
+    while (pl.seg % pl.anchor != 0) pl.anchor -= 64;  // (64 divides it)
   }
   pl.own_anchors = decay_grad && !(pl.segmented && pl.anchor == pl.seg);
   pl.anchored = decay_grad ? kda::linear_slots(total_tokens, num_seqs, pl.anchor) : 0;
