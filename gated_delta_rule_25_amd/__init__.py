@@ -126,6 +126,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _check(t, name, shape, dtype, device):
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if tuple(t.shape) != tuple(shape):

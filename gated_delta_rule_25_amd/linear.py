@@ -258,7 +258,7 @@ def linear_decode_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     dev, dt = q.device, q.dtype
     _check(state, "state", (n, h, D, D), torch.float32, dev)
     if out is None:
-        out = torch.empty((n, h, D), dtype=dt, device=dev)
+        out = torch.empty_like(v)
     else:
         _check(out, "out", (n, h, D), dt, dev)
     with _on(dev):
