@@ -1093,12 +1093,12 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
 template <typename E, int NW, bool REV, bool OUT>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  // Blocks b and b + 8 run on the same XCD: what a head's column blocks both
-  // read comes from its L2 the second time.
+  // Blocks b and b + 8 run on the same XCD: what the column blocks of a head and
+  // the heads that share a key head read comes from its L2 after the first.
   constexpr int CB = 8 / NW;
-  const int64_t slot8 = blockIdx.x >> 3, u = p.unit0 + slot8 / CB * 8 + (blockIdx.x & 7);
-  const int cb = (int)(slot8 % CB);
-  if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, cb);
+  const int share = p.num_heads / p.k_heads, per = share * CB;
+  const int64_t slot8 = blockIdx.x >> 3, u = p.unit0 + (slot8 / per * 8 + (blockIdx.x & 7)) * share + slot8 % per / CB;
+  if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, (int)(slot8 % CB));
 }
 
 // The three gradients' walks of every work item: per sequence (or segment) the
@@ -1158,11 +1158,12 @@ hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
   hipError_t e = allow_lds(linear_walk_kernel<E, NW, REV, OUT>, LDS, set);
   if (e != hipSuccess) return e;
   constexpr int CB = 8 / NW, THREADS = 64 * (NW + 4);
-  constexpr int64_t MOST = kMaxThreads / THREADS / (8 * CB) * 8;  // units of a launch
+  const int64_t group = 8 * (a.num_heads / a.k_heads);                             // units that go to the XCDs together
+  const int64_t most = std::max(kMaxThreads / THREADS / (group * CB), (int64_t)1) * group;  // units of a launch
   LinearWalkArgs part = a;
-  for (part.unit0 = 0; part.unit0 < a.units; part.unit0 += MOST) {
-    part.units = std::min(a.units, part.unit0 + MOST);
-    const int64_t blocks = (part.units - part.unit0 + 7) / 8 * 8 * CB;
+  for (part.unit0 = 0; part.unit0 < a.units; part.unit0 += most) {
+    part.units = std::min(a.units, part.unit0 + most);
+    const int64_t blocks = (part.units - part.unit0 + group - 1) / group * group * CB;
     hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, OUT>), dim3((unsigned)blocks), dim3(THREADS), LDS, stream, part);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
