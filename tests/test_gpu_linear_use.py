@@ -5,6 +5,8 @@ with padding, with many and skewed sequences, and all of it together.
 Tolerances are those of tests/linear_testlib.py and tests/test_gpu_beam.py;
 what runs the same kernels twice is compared bit for bit.
 """
+import gc
+
 import pytest
 import torch
 
@@ -402,6 +404,7 @@ def test_captured_backward_refuses_accumulators_from_elsewhere(monkeypatch):
     torch.cuda.synchronize()
     assert all(t.grad is None for t in x)
     del alive, o, loss, _
+    gc.collect()  # the refusal's traceback holds its frames, and they the graph
     with torch.cuda.stream(side):
         o, _ = kda.chunk_linear(*x)
         with monkeypatch.context() as m:
