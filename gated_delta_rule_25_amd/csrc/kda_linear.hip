@@ -1090,15 +1090,38 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   }
 }
 
-template <typename E, int NW, bool REV, bool OUT>
+// Blocks b and b + 8 run on the same XCD: what the column blocks of a head and
+// the heads that share a key head read comes from its L2 after the first.
+template <int CB>
+__device__ __forceinline__ int64_t unit_of(const LinearWalkArgs& p, int64_t block, int& cb) {
+  const int share = p.num_heads / p.k_heads, per = share * CB;
+  const int64_t slot8 = block >> 3;
+  cb = (int)(slot8 % CB);
+  return p.unit0 + (slot8 / per * 8 + (block & 7)) * share + slot8 % per / CB;
+}
+
+template <typename E, int NW>
 __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(const LinearWalkArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  // Blocks b and b + 8 run on the same XCD: what the column blocks of a head and
-  // the heads that share a key head read comes from its L2 after the first.
-  constexpr int CB = 8 / NW;
-  const int share = p.num_heads / p.k_heads, per = share * CB;
-  const int64_t slot8 = blockIdx.x >> 3, u = p.unit0 + (slot8 / per * 8 + (blockIdx.x & 7)) * share + slot8 % per / CB;
-  if (u < p.units) walk<E, NW, REV, false, OUT, false>(p, smem, u, (int)(slot8 % CB));
+  int cb;
+  const int64_t u = unit_of<8 / NW>(p, blockIdx.x, cb);
+  if (u < p.units) walk<E, NW, false, false, true, false>(p, smem, u, cb);
+}
+
+// Every segment's own contribution to the state, forwards and, in the second
+// half of the blocks if there are any, backwards.
+template <typename E>
+__global__ __launch_bounds__(64 * (8 + 4)) void linear_states_kernel(const LinearWalkArgs f, const LinearWalkArgs r,
+                                                                    unsigned forward_blocks) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  int cb;
+  if (blockIdx.x < forward_blocks) {
+    const int64_t u = unit_of<1>(f, blockIdx.x, cb);
+    if (u < f.units) walk<E, 8, false, false, false, false>(f, smem, u, cb);
+  } else {
+    const int64_t u = unit_of<1>(r, blockIdx.x - forward_blocks, cb);
+    if (u < r.units) walk<E, 8, true, false, false, false>(r, smem, u, cb);
+  }
 }
 
 // The three gradients' walks of every work item: per sequence (or segment) the
@@ -1151,30 +1174,48 @@ hipError_t allow_lds(K kernel, int bytes, std::atomic<bool> (&set)[64]) {
   return e;
 }
 
-template <typename E, int NW, bool REV, bool OUT>
-hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
-  constexpr int LDS = WalkLayout<E, NW, false, false>::BYTES;
-  static std::atomic<bool> set[64];
-  hipError_t e = allow_lds(linear_walk_kernel<E, NW, REV, OUT>, LDS, set);
-  if (e != hipSuccess) return e;
-  constexpr int CB = 8 / NW, THREADS = 64 * (NW + 4);
-  const int64_t group = 8 * (a.num_heads / a.k_heads);                             // units that go to the XCDs together
-  const int64_t most = std::max(kMaxThreads / THREADS / (group * CB), (int64_t)1) * group;  // units of a launch
-  LinearWalkArgs part = a;
-  for (part.unit0 = 0; part.unit0 < a.units; part.unit0 += most) {
-    part.units = std::min(a.units, part.unit0 + most);
-    const int64_t blocks = (part.units - part.unit0 + group - 1) / group * group * CB;
-    hipLaunchKernelGGL((linear_walk_kernel<E, NW, REV, OUT>), dim3((unsigned)blocks), dim3(THREADS), LDS, stream, part);
-    e = hipGetLastError();
+// Calls launch(first unit, units behind the last, blocks) for parts of a.units
+// whose blocks make no more than `most_blocks`.
+template <int CB, typename F>
+hipError_t launch_parts(const LinearWalkArgs& a, int64_t most_blocks, const F& launch) {
+  const int64_t group = 8 * (a.num_heads / a.k_heads);  // units that go to the XCDs together
+  const int64_t most = std::max(most_blocks / (group * CB), (int64_t)1) * group;
+  for (int64_t u = 0; u < a.units; u += most) {
+    const int64_t end = std::min(a.units, u + most);
+    launch(u, end, (unsigned)((end - u + group - 1) / group * group * CB));
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
+template <typename E, int NW>
+hipError_t launch_walk_t(const LinearWalkArgs& a, hipStream_t stream) {
+  constexpr int LDS = WalkLayout<E, NW, false, false>::BYTES, THREADS = 64 * (NW + 4);
+  static std::atomic<bool> set[64];
+  hipError_t e = allow_lds(linear_walk_kernel<E, NW>, LDS, set);
+  if (e != hipSuccess) return e;
+  return launch_parts<8 / NW>(a, kMaxThreads / THREADS, [&](int64_t u, int64_t end, unsigned blocks) {
+    LinearWalkArgs part = a;
+    part.unit0 = u;
+    part.units = end;
+    hipLaunchKernelGGL((linear_walk_kernel<E, NW>), dim3(blocks), dim3(THREADS), LDS, stream, part);
+  });
+}
+
 template <typename E>
-hipError_t launch_walk_e(const LinearWalkArgs& a, hipStream_t stream) {
-  if (!a.write_o) return a.reverse ? launch_walk_t<E, 8, true, false>(a, stream) : launch_walk_t<E, 8, false, false>(a, stream);
-  return a.narrow ? launch_walk_t<E, 4, false, true>(a, stream) : launch_walk_t<E, 8, false, true>(a, stream);
+hipError_t launch_states_e(const LinearWalkArgs& forward, const LinearWalkArgs* reverse, hipStream_t stream) {
+  constexpr int LDS = WalkLayout<E, 8, false, false>::BYTES, THREADS = 64 * (8 + 4);
+  static std::atomic<bool> set[64];
+  hipError_t e = allow_lds(linear_states_kernel<E>, LDS, set);
+  if (e != hipSuccess) return e;
+  return launch_parts<1>(forward, kMaxThreads / THREADS / 2, [&](int64_t u, int64_t end, unsigned blocks) {
+    LinearWalkArgs f = forward, r = reverse ? *reverse : forward;
+    f.unit0 = r.unit0 = u;
+    f.units = r.units = end;
+    hipLaunchKernelGGL(linear_states_kernel<E>, dim3(reverse ? 2 * blocks : blocks), dim3(THREADS), LDS, stream, f, r,
+                       blocks);
+  });
 }
 
 template <typename E, int NW, bool DG>
@@ -1302,11 +1343,11 @@ __device__ __forceinline__ void decay_grad(const LinearDecayGradArgs& a) {
 // contribution while it composes this one.
 // ---------------------------------------------------------------------------
 template <bool REV>
-__global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a) {
+__device__ __forceinline__ void scan(const LinearScanArgs& a, int64_t block) {
   constexpr size_t kState = (size_t)D * D;
   const int H = a.num_heads;
-  const int64_t nh = a.unit0 + (blockIdx.x >> 4);
-  const int at = ((int)(blockIdx.x & 15) * 256 + threadIdx.x) * 4;
+  const int64_t nh = a.unit0 + (block >> 4);
+  const int at = ((int)(block & 15) * 256 + threadIdx.x) * 4;
   const int n = (int)(nh / H), h = (int)(nh % H);
   int64_t bos, eos;
   seq_range(a.cu, n, a.total_tokens, bos, eos);
@@ -1331,6 +1372,12 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a
     *reinterpret_cast<f32x4*>(a.snap + where(j) * kState + at) = s;
     s = s * d + add;
   }
+}
+
+__global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs f, const LinearScanArgs r,
+                                                          unsigned forward_blocks) {
+  if (blockIdx.x < forward_blocks) scan<false>(f, blockIdx.x);
+  else scan<true>(r, blockIdx.x - forward_blocks);
 }
 
 // ---------------------------------------------------------------------------
@@ -1376,7 +1423,12 @@ __global__ __launch_bounds__(64) void linear_decay_sum_kernel(const double* __re
 }  // namespace
 
 hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream) {
-  return a.bf16 ? launch_walk_e<__bf16>(a, stream) : launch_walk_e<float>(a, stream);
+  if (a.narrow) return a.bf16 ? launch_walk_t<__bf16, 4>(a, stream) : launch_walk_t<float, 4>(a, stream);
+  return a.bf16 ? launch_walk_t<__bf16, 8>(a, stream) : launch_walk_t<float, 8>(a, stream);
+}
+
+hipError_t launch_linear_states(const LinearWalkArgs& f, const LinearWalkArgs* r, hipStream_t stream) {
+  return f.bf16 ? launch_states_e<__bf16>(f, r, stream) : launch_states_e<float>(f, r, stream);
 }
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream) {
@@ -1394,14 +1446,14 @@ hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t strea
   return hipGetLastError();
 }
 
-hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream) {
-  const int64_t units = (int64_t)a.num_seqs * a.num_heads;
-  constexpr int64_t MOST = kMaxThreads / 256 / 16;
-  LinearScanArgs part = a;
-  for (part.unit0 = 0; part.unit0 < units; part.unit0 += MOST) {
-    const dim3 grid((unsigned)(std::min(units - part.unit0, MOST) * 16));
-    if (a.reverse) hipLaunchKernelGGL(linear_scan_kernel<true>, grid, dim3(256), 0, stream, part);
-    else hipLaunchKernelGGL(linear_scan_kernel<false>, grid, dim3(256), 0, stream, part);
+hipError_t launch_linear_scan(LinearScanArgs f, const LinearScanArgs* reverse, hipStream_t stream) {
+  const int64_t units = (int64_t)f.num_seqs * f.num_heads;
+  constexpr int64_t MOST = kMaxThreads / 256 / 32;
+  LinearScanArgs r = reverse ? *reverse : f;
+  for (int64_t u = 0; u < units; u += MOST) {
+    f.unit0 = r.unit0 = u;
+    const unsigned blocks = (unsigned)(std::min(units - u, MOST) * 16);
+    hipLaunchKernelGGL(linear_scan_kernel, dim3(reverse ? 2 * blocks : blocks), dim3(256), 0, stream, f, r, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

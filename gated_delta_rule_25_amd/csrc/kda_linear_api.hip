@@ -59,11 +59,11 @@ struct LinearPlan {
 // 131072 tokens: 380 us in segments of 4096, 448 at 1024, 3726 in one walk; 96
 // heads x 8192: 225 us in one walk of half heads, 300 at 1536); half heads
 // when chains are fewer than units.
-// Backward, three walks a chain: segments, one per unit, from six units per
-// chain on (32 heads x 8192 tokens: 308 us in segments of 1024, 345 at 512,
-// 359 in one walk of half heads, 443 of whole ones; 48 heads: 477, 508, 489,
-// 495).  With more chains one walk each: whole heads if all chains are as long
-// (96 heads x 8192: 757-847 us, half heads 975, segments of 1024 870).  The
+// Backward, three walks a chain: segments, one per unit, from five units per
+// chain on (32 heads x 8192 tokens: 280 us in segments of 1024, 320 at 512, 333
+// in one walk of half heads; 48 heads: 443, 497 and 493 in one walk of whole
+// ones; 64 heads: 570, 633, 512).  With more chains one walk each: whole heads if all chains are as long
+// (96 heads x 8192: 700-727 us, half heads 975, segments of 1024 855).  The
 // lengths of several sequences are not known here, and the longest one is
 // waited for: half heads until two rounds of the card are full (9 sequences of
 // up to 2900 tokens x 16 heads: 157 us, whole heads 206; of up to 1200: 103
@@ -71,7 +71,7 @@ struct LinearPlan {
 void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
                      bool backward) {
   const int64_t units = (int64_t)num_seqs * num_heads;
-  const bool few = (backward ? 6 : 3) * units < cus;
+  const bool few = (backward ? 5 : 3) * units < cus;
   if (segment_tokens > 0) {
     pl.segmented = true;
     pl.seg = segment_tokens;
@@ -139,7 +139,8 @@ LinearPlan make_fwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
 
 // Pieces, each 256-byte aligned: segmented, S and dS at the segment
 // boundaries ([slots][H] states); both at the boundaries of the decays'
-// gradient where those are others; the segments' decays [slots][H]; r_t and
+// gradient where those are others; the segments' decays [slots][H], once
+// for each direction (the same but for the order of their sums); r_t and
 // c_t [column blocks][H][T]; the stretches' sums of a constant decay's
 // gradient; the fp32 gradients [T, H, 128] that shared heads are summed from.
 LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int num_qk_heads, int segment_tokens,
@@ -167,7 +168,7 @@ LinearPlan make_bwd_plan(int num_seqs, int64_t total_tokens, int num_heads, int 
   pl.off_anchor = off;
   off += 2 * (size_t)pl.boundaries * num_heads * kStateBytes;
   pl.off_decay = off;
-  if (pl.segmented) off += align256(units * sizeof(float));
+  if (pl.segmented) off += align256(2 * units * sizeof(float));
   pl.off_change = off;
   if (decay_grad) off += align256(2 * pl.blocks * rows * sizeof(float));
   pl.off_part = off;
@@ -205,24 +206,27 @@ bool any_overlap(const Range* outs, size_t no, const Range* ins, size_t ni) {
   return false;
 }
 
-// Incoming states of the segments: their own contributions, then the scan.
-hipError_t segment_states(kda::LinearWalkArgs w, const float* init, hipStream_t stream) {
-  w.write_o = false;
-  w.narrow = false;
-  hipError_t e = kda::launch_linear_walk(w, stream);
+// Incoming states of the segments: their own contributions, then the scan;
+// forwards and, if `r` is given, backwards beside it.
+hipError_t segment_states(const kda::LinearWalkArgs& f, const kda::LinearWalkArgs* r, hipStream_t stream) {
+  hipError_t e = kda::launch_linear_states(f, r, stream);
   if (e != hipSuccess) return e;
-  kda::LinearScanArgs s;
-  std::memset(&s, 0, sizeof(s));
-  s.snap = w.snap;
-  s.seg_decay = w.seg_decay;
-  s.init = init;
-  s.cu = w.cu;
-  s.num_seqs = w.num_seqs;
-  s.total_tokens = w.total_tokens;
-  s.num_heads = w.num_heads;
-  s.seg = w.seg;
-  s.reverse = w.reverse;
-  return kda::launch_linear_scan(s, stream);
+  auto scan_of = [](const kda::LinearWalkArgs& w) {
+    kda::LinearScanArgs s;
+    std::memset(&s, 0, sizeof(s));
+    s.snap = w.snap;
+    s.seg_decay = w.seg_decay;
+    s.init = w.init;
+    s.cu = w.cu;
+    s.num_seqs = w.num_seqs;
+    s.total_tokens = w.total_tokens;
+    s.num_heads = w.num_heads;
+    s.seg = w.seg;
+    return s;
+  };
+  kda::LinearScanArgs back;
+  if (r) back = scan_of(*r);
+  return kda::launch_linear_scan(scan_of(f), r ? &back : nullptr, stream);
 }
 
 }  // namespace
@@ -298,14 +302,13 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
   w.segmented = pl.segmented;
   w.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
   w.narrow = pl.narrow;
-  w.write_o = true;
   w.init = initial_state;
   w.fin = final_state;
   w.o = o;
   if (pl.segmented) {
     w.snap = reinterpret_cast<float*>(ws + pl.off_fsnap);
     w.seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
-    if (segment_states(w, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
+    if (segment_states(w, nullptr, stream) != hipSuccess) return KDA_ERR_HIP;
   }
   return kda::launch_linear_walk(w, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
@@ -398,7 +401,6 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   base.narrow = pl.narrow;
   base.units = (pl.segmented ? pl.slots : (int64_t)num_seqs) * num_heads;
   base.seg_decay = reinterpret_cast<float*>(ws + pl.off_decay);
-  base.write_o = true;
   const int hq = num_qk_heads, hv = num_heads;
   auto role = [](kda::LinearWalkArgs w, const void* a, int ah, const void* b, int bh, const void* c, int ch) {
     w.q = a;
@@ -424,7 +426,6 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   g.dq.change = change;
   g.dq.o = shared ? static_cast<void*>(share) : dq;
   g.dq.o_f32 = shared;
-  base.reverse = true;
   base.init = d_final_state;
   base.snap = rsnap;
   g.dk = role(base, v, hv, d_o, hv, q, hq);
@@ -439,8 +440,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   g.dv.o = dv;
   if (pl.segmented) {
     kda::LinearWalkArgs f = role(g.dq, nullptr, hq, k, hq, v, hv);
-    if (segment_states(f, initial_state, stream) != hipSuccess) return KDA_ERR_HIP;
-    if (segment_states(g.dv, d_final_state, stream) != hipSuccess) return KDA_ERR_HIP;
+    kda::LinearWalkArgs r = g.dv;
+    r.seg_decay += (size_t)pl.slots * num_heads;
+    if (segment_states(f, &r, stream) != hipSuccess) return KDA_ERR_HIP;
   }
   if (kda::launch_linear_grad(g, stream) != hipSuccess) return KDA_ERR_HIP;
   kda::LinearFinishArgs f;

@@ -51,8 +51,6 @@ struct LinearWalkArgs {
   bool segmented;          // work items are (segment, head), else (sequence, head)
   int64_t units;           // work items
   int64_t unit0;           // first item of the launch (set by it)
-  bool reverse;            // backwards in time
-  bool write_o;            // false: only each segment's own contribution to the state
   bool narrow;             // 64 value columns per workgroup instead of 128
   const float* init;       // [N,H,128,128] or null (zero): enters at the sequence's first (reverse: last) token
   float* fin;              // [N,H,128,128] or null: the state behind the last (reverse: before the first) token
@@ -125,7 +123,6 @@ struct LinearScanArgs {
   int64_t total_tokens;
   int num_heads;
   int seg;
-  bool reverse;
 };
 
 struct LinearDecodeArgs {
@@ -143,9 +140,12 @@ struct LinearDecodeArgs {
 };
 
 hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t stream);
+// Segments: their own contributions to the state and, by the scan, the states
+// that enter them; forwards and, if given, backwards.
+hipError_t launch_linear_states(const LinearWalkArgs& f, const LinearWalkArgs* r, hipStream_t stream);
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream);
 hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t stream);
-hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t stream);
+hipError_t launch_linear_scan(LinearScanArgs f, const LinearScanArgs* r, hipStream_t stream);
 hipError_t launch_linear_decay_sum(const double* part, float* dst, int64_t units, int num_heads, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearDecodeArgs& a, hipStream_t stream);
 // Checks the documented input ranges (log_decay <= 0 and not NaN; cu_seqlens)

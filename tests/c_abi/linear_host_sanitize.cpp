@@ -45,15 +45,27 @@ hipError_t launch_linear_walk(const LinearWalkArgs& a, hipStream_t) {
     const size_t slots = (size_t)linear_slots(a.total_tokens, a.num_seqs, a.seg) * a.num_heads;
     EXPECT((size_t)a.units == slots);
     inside(a.snap, slots * kState);
-    inside(a.seg_decay, slots * 4);
   } else {
     EXPECT(a.units == (int64_t)a.num_seqs * a.num_heads);
   }
   return hipSuccess;
 }
-hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t) {
+hipError_t launch_linear_states(const LinearWalkArgs& f, const LinearWalkArgs* r, hipStream_t) {
   ++launches;
-  inside(a.snap, (size_t)linear_slots(a.total_tokens, a.num_seqs, a.seg) * a.num_heads * kState);
+  const size_t slots = (size_t)linear_slots(f.total_tokens, f.num_seqs, f.seg) * f.num_heads;
+  EXPECT(f.segmented && (size_t)f.units == slots && (!r || (r->segmented && r->units == f.units && r->snap != f.snap)));
+  inside(f.seg_decay, slots * 4);
+  if (r) {
+    inside(r->seg_decay, slots * 4);
+    EXPECT(r->seg_decay >= f.seg_decay + slots);
+  }
+  return hipSuccess;
+}
+hipError_t launch_linear_scan(LinearScanArgs f, const LinearScanArgs* r, hipStream_t) {
+  ++launches;
+  const size_t slots = (size_t)linear_slots(f.total_tokens, f.num_seqs, f.seg) * f.num_heads;
+  inside(f.snap, slots * kState);
+  if (r) inside(r->snap, slots * kState);
   return hipSuccess;
 }
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t) {

@@ -128,8 +128,8 @@ def test_chunk_workspaces(lib):
     assert f(1, 1000, 4, 2, 128, 128, 9, 64) == 0
     assert f(1, 1 << 31, 4, 2, 128, 128, BF16, 64) == 0
     # backward without the decays' gradient: the states of both directions, decays, and the shared heads' fp32 sums
-    assert b(1, 1000, 4, 4, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512
-    assert b(1, 1000, 4, 2, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 512 + 2 * 1000 * 4 * 128 * 4
+    assert b(1, 1000, 4, 4, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 768
+    assert b(1, 1000, 4, 2, 0, 0, 1, 128, 128, BF16, 64) == 2 * 17 * 4 * state + 768 + 2 * 1000 * 4 * 128 * 4
     assert b(1, 1000, 4, 4, 0, 0, 1, 128, 128, BF16, -1) == 0
     # with it, r and c per token, and one state of each direction per boundary: short sequences have none but
     # their ends, and those only where a gradient arrives there (r and c of two halves of a head with few chains)
