@@ -97,7 +97,8 @@ size_t kda_linear_chunk_bwd_workspace_bytes(int num_seqs, int64_t total_tokens, 
  *   d_initial_state [N, H, 128, 128] fp32 or NULL (not written)
  *
  * It needs only the forward's inputs; no output may overlap an input, another
- * output or the workspace.
+ * output or the workspace.  With d_log_decay, total_tokens * num_heads / 1024
+ * (a constant decay: / 256) + 2 * num_seqs * num_heads is at most 14 * 2^20.
  */
 kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                                 const float* initial_state, const int32_t* cu_seqlens, const void* d_o,
@@ -107,7 +108,8 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
                                 float* d_initial_state, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
- * One token for N independent sequences, the states advanced in place.
+ * One token for N independent sequences, the states advanced in place
+ * (num_seqs * num_heads below 2^24).
  *
  *   state      [N, H, 128, 128] fp32, 16-byte aligned
  *   q, k       [N, num_qk_heads, 128] dtype;  v, o  [N, H, 128] dtype
