@@ -291,7 +291,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
   w.q_heads = w.k_heads = num_qk_heads;
   w.v_heads = w.x_heads = num_heads;
   w.log_decay = log_decay;
-  w.decay_per_head = decay_per_head != 0;
+  w.decay_per_head = decay_per_head != 0 && total_tokens > 0;  // (without tokens there may be no decays to read)
   w.cu = cu_seqlens;
   w.num_seqs = num_seqs;
   w.total_tokens = total_tokens;
@@ -388,7 +388,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
   kda::LinearWalkArgs base;
   std::memset(&base, 0, sizeof(base));
   base.log_decay = log_decay;
-  base.decay_per_head = per_head;
+  base.decay_per_head = per_head && total_tokens > 0;  // (without tokens there may be no decays to read)
   base.cu = cu_seqlens;
   base.num_seqs = num_seqs;
   base.total_tokens = total_tokens;
