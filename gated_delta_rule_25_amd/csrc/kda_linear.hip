@@ -1435,10 +1435,16 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream) {
   return a.dq.bf16 ? launch_grad_e<__bf16>(a, stream) : launch_grad_e<float>(a, stream);
 }
 
+// Workgroups for the sums of dq, and as many for dk, over shared heads (they go
+// on by strides): with the 14 * 2^20 stretches that a call may have at most
+// (kda_linear_api.hip), 2^24 - 2 of 256 threads.
+constexpr int64_t kMostShareBlocks = ((int64_t)1 << 20) - 1;
+static_assert((((int64_t)14 << 20) + 2 * kMostShareBlocks) * 256 <= kMaxThreads, "one launch holds both");
+
 hipError_t launch_linear_finish(LinearFinishArgs a, bool bf16, hipStream_t stream) {
   const LinearDecayGradArgs& d = a.decay;
   a.decay_blocks = a.decay_blocks ? linear_slots(d.total_tokens, d.num_seqs, d.anchor) * d.num_heads : 0;
-  a.share_blocks = a.share ? std::min((d.total_tokens * a.qk_heads * 32 + 255) / 256, (int64_t)1 << 20) : 0;
+  a.share_blocks = a.share ? std::min((d.total_tokens * a.qk_heads * 32 + 255) / 256, kMostShareBlocks) : 0;
   const int64_t blocks = a.decay_blocks + 2 * a.share_blocks;
   if (blocks == 0) return hipSuccess;
   if (bf16) hipLaunchKernelGGL(linear_finish_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, stream, a);

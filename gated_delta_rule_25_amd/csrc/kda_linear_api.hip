@@ -118,7 +118,7 @@ int whole_dv_heads(int heads, bool decay_grad, int cus) {
 
 bool plan_ok(const LinearPlan& pl, int num_heads) {
   // (one workgroup of 256 threads per stretch in a launch of below 2^32 threads,
-  // beside 2^21 others)
+  // beside fewer than 2^21 others: kMostShareBlocks)
   return pl.slots * num_heads <= (int64_t)INT32_MAX / 4 && pl.anchored * num_heads <= (int64_t)14 << 20;
 }
 

@@ -128,9 +128,42 @@ static void no_tokens() {
         }
 }
 
+// The last launch of the backward pass has a workgroup for each stretch of the
+// decays' gradient and up to 2^20 for the sums of dq and as many for dk over
+// shared heads; both at their limit, which the header gives as 14 * 2^20 for
+// the former: tokens * heads / 1024 (/ 256) + 2 * sequences * heads.
+static void most_stretches() {
+  const Sizes at_limit[] = {{458240, 1 << 20, 16, 8, 0, -1}, {456704, 1 << 20, 16, 8, 1, -1}, {458240, 1 << 20, 16, 16, 0, -1}};
+  for (const Sizes& z : at_limit) {
+    EXPECT(z.t * z.h / (z.per_head ? 256 : 1024) + 2ll * z.n * z.h == 14ll << 20);
+    EXPECT(backward(z, P<float>(3)) == KDA_OK);
+    Sizes over = z;
+    over.n += 1;
+    EXPECT(backward(over, P<float>(3)) == KDA_ERR_INVALID_ARG);
+  }
+}
+
+// Sizes from one token to the largest, every schedule.
+static void sizes() {
+  for (int n : {1, 2, 9, 1000, 400000})
+    for (int h : {1, 3, 16, 48, 90, 96, 300, 65535})
+      for (int64_t t : {1ll, 63ll, 4927ll, 131072ll, 3000000ll, 2147483647ll})
+        for (int segment : {-1, 0, 64, 64 * 1021})
+          for (int hq : {1, h})
+            for (int per_head : {0, 1}) {
+              const Sizes z = {n, t, h, hq, per_head, segment};
+              if ((double)t * h > 1e9 || forward_bytes(z) >= 1ull << 40) continue;  // (2 TiB between the tensors)
+              const int f = forward(z, P<float>(3)), b = backward(z, P<float>(3));
+              EXPECT(f == KDA_OK || f == KDA_ERR_INVALID_ARG);
+              EXPECT(b == KDA_OK || b == KDA_ERR_INVALID_ARG);
+            }
+}
+
 int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "no_tokens") no_tokens();
+  else if (what == "most_stretches") most_stretches();
+  else if (what == "sizes") sizes();
   else EXPECT(!"a known check");
   EXPECT(launches > 0);
   if (failures == 0) std::printf("%d launches checked\n", launches);

@@ -40,3 +40,10 @@ def test_calls_without_tokens(program):
     """Such calls take NULL for the tensors of tokens; no kernel may be given
     a constant decay to read at NULL."""
     check(program, "no_tokens")
+
+
+@pytest.mark.parametrize("what", ["most_stretches", "sizes"])
+def test_launches_have_fewer_threads_than_the_runtime_takes(program, what):
+    """Fewer than 2^32 a launch, at the sizes the header gives as the largest
+    and below them."""
+    check(program, what)
