@@ -89,6 +89,23 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     return new_scores, tokens, parents, new_finished
 
 
+def _refuse_reorder(ranges, parents) -> None:
+    """Refuses, before any of them is moved, the tensors that kda_beam_reorder
+    would refuse in a later one of several calls.  ranges: (address, bytes,
+    bytes of a row) of each state; parents: its (address, bytes)."""
+    used = sorted((a, a + n) for a, n, _ in [*ranges, (*parents, 0)] if n > 0)
+    for (_, end), (begin, _) in zip(used, used[1:]):
+        if begin < end:
+            raise ValueError("the states and parents must not overlap")
+    for i in range(0, len(ranges), BEAM_REORDER_MAX):
+        blocks = 0
+        for a, _, row in ranges[i:i + BEAM_REORDER_MAX]:
+            unit = 16 if (a | row) % 16 == 0 else 4 if (a | row) % 4 == 0 else 1
+            blocks += (row // unit + 255) // 256
+        if blocks * 256 > 2 ** 32 - 1:
+            raise ValueError("the states' rows are too long")
+
+
 def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: torch.Tensor):
     """Rows of the states follow the selected parents, in place
     (kda_beam_reorder): row b * K + k becomes what row b * K + parents[b, k]
@@ -110,6 +127,7 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
     _check(parents, "parents", (b, k), torch.int32, dev)
     if not many:
         raise ValueError("no states")
+    held = []  # (address, bytes, bytes of a row)
     for t in many:
         if not isinstance(t, torch.Tensor):
             raise TypeError("states must be torch.Tensors")
@@ -119,15 +137,19 @@ def beam_reorder(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: t
             raise ValueError("a state is on %s, expected %s" % (t.device, dev))
         if not t.is_contiguous():
             raise ValueError("states must be contiguous")
+        n = t.nbytes
+        held.append((t.data_ptr(), n, n // (b * k) if b * k else 0))
     if len(many) > 1:
-        held = [t.data_ptr() for t in many if t.numel()]
-        if len(set(held)) != len(held):
+        at = [a for a, n, _ in held if n]
+        if len(set(at)) != len(at):
             raise ValueError("the same state is given twice")
+    if len(many) > BEAM_REORDER_MAX:
+        _refuse_reorder(held, (parents.data_ptr(), parents.nbytes))
     with _on(dev):
         for i in range(0, len(many), BEAM_REORDER_MAX):
-            part = many[i:i + BEAM_REORDER_MAX]
-            ptrs = (ctypes.c_void_p * len(part))(*[t.data_ptr() for t in part])
-            rows = (ctypes.c_int64 * len(part))(*[t.nbytes // (b * k) if b * k else 0 for t in part])
+            part = held[i:i + BEAM_REORDER_MAX]
+            ptrs = (ctypes.c_void_p * len(part))(*[a for a, _, _ in part])
+            rows = (ctypes.c_int64 * len(part))(*[r for _, _, r in part])
             rc = lib.kda_beam_reorder(ptrs, rows, len(part), _ptr(parents), b, k, _stream(dev))
             if rc != KDA_OK:
                 raise KDAError(rc, "kda_beam_reorder")
