@@ -284,12 +284,13 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
       const int sl = min(lane, a.plan.slices - 1);
       const float sm = lane < a.plan.slices ? a.slice_max[row * a.plan.slices + sl] : -INFINITY;
       const float ssum = lane < a.plan.slices ? a.slice_sum[row * a.plan.slices + sl] : 0.f;
-      // log of the row's sum of exponentials
+      // log of the row's sum of exponentials, relative to its largest logit
+      // (which may be so large that the sum of the two is no more than itself)
       const float m = wave_fmax(sm);
       double sum = sm > -INFINITY ? (double)ssum * exp((double)sm - (double)m) : 0.0;
 #pragma unroll
       for (int i = 32; i >= 1; i >>= 1) sum += __shfl_xor(sum, i);
-      const double lse = (double)m + log(sum);
+      const double log_sum = log(sum);
       // a bound that C parts reach
       float most = -INFINITY;
 #pragma unroll
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
         least = __shfl((unsigned long long)list, C - 1);
       }
       const float v = key_value(list);
-      if (v > -INFINITY) mine = (double)score + ((double)v - lse);
+      if (v > -INFINITY) mine = (double)score + (((double)v - (double)m) - log_sum);
       at = (uint64_t)k << 32 | key_at(list);
     }
     if (!(mine == mine)) mine = -INFINITY;  // a score that is not a number

@@ -26,3 +26,24 @@ def test_refused_reorder_of_many_states_moves_none(last):
     torch.cuda.synchronize()
     at = torch.tensor([1, 0, 0, 5, 5, 4], device=DEV)
     assert all(torch.equal(x, y[at]) for x, y in zip(states, before))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("top", [1e6, 1e18, 3e38, float("inf")])
+@pytest.mark.parametrize("n", [1, 2, 3])
+def test_select_of_large_equal_logits(dtype, top, n):
+    """n tokens at a large logit and nothing near it: each has 1 / n of the
+    beam's probability (+inf counts as the largest finite number).  Scores are
+    rounded once, and the sum of exponentials is off by at most 2^-20."""
+    x = torch.zeros(1, 2, 300, dtype=dtype, device=DEV)
+    at = [7, 100, 299][:n]
+    x[0, :, at] = top
+    s = torch.tensor([[-0.5, -1.5]], device=DEV)
+    scores, tokens, parents, _ = kda.beam_select(x, s)
+    torch.cuda.synchronize()
+    log_n = torch.tensor(float(n), dtype=torch.float64).log()
+    want = [(-0.5, 0, 7), (-1.5, 1, 7)] if n == 1 else [(-0.5, 0, 7), (-0.5, 0, 100)]
+    for i, (score, beam, token) in enumerate(want):
+        w = float(score - log_n)
+        assert abs(float(scores[0, i]) - w) <= 2.0 ** -24 * abs(w) + 2.0 ** -20
+        assert (int(parents[0, i]), int(tokens[0, i])) == (beam, token)
