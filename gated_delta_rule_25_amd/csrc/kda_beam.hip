@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
   __shared__ uint64_t few_key[kBeamMax][64];
   __shared__ int few_id[kBeamMax][64];
   __shared__ double cand_score[kBeamMax * kBeamMax];
-  __shared__ uint64_t cand_at[kBeamMax * kBeamMax];  // beam << 32 | token: the order of beam * vocab + token
+  __shared__ uint32_t cand_token[kBeamMax * kBeamMax];
   __shared__ uint8_t done[kBeamMax];
   const float score = a.scores[row];
   const bool fin = a.finished && a.finished[row];
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
   const int parts = a.plan.slices * kBeamThreads;
   {
     double mine = -INFINITY;  // lane i < C: the row's i-th best
-    uint64_t at = 0;
+    uint32_t token = 0;
     if (!row_is_read(a, row)) {
       // the end token if the beam is finished (a beam without a score ties at
       // -inf with everything), then the lowest tokens at -inf
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
       int t = lane;
       if (ends) t = lane == 0 ? a.end_token : (lane - 1 < a.end_token ? lane - 1 : lane);
       if (ends && lane == 0) mine = (double)score;
-      at = (uint64_t)k << 32 | (uint32_t)t;
+      token = (uint32_t)t;
     } else {
       // all loads before the first use: they are in flight together
       const float* pm = a.part_max + row * parts;
@@ -421,35 +421,35 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
       }
       const float v = key_value(list);
       if (v > -INFINITY) mine = (double)score + (((double)v - (double)m) - log_sum);
-      at = (uint64_t)k << 32 | key_at(list);
+      token = key_at(list);
     }
     if (!(mine == mine)) mine = -INFINITY;  // a score that is not a number
     if (lane < C) {
       cand_score[k * C + lane] = mine;
-      cand_at[k * C + lane] = at;
+      cand_token[k * C + lane] = token;
     }
     if (lane == 0) done[k] = fin;
   }
   __syncthreads();
   // the K best of the K x C candidates (C = K, or V < K candidates a row): a
-  // candidate's place is the number of better ones, the largest score first,
-  // then the lowest index with it.  Wave k places its own row's, each by 8
-  // lanes (4 with more than 8 beams).
+  // candidate's place is the number of better ones, the largest score first.
+  // Among equal scores the lower beam comes first, and within a beam its list's
+  // order, which is that of the logits: logits that differ may well have the
+  // same score.  Wave k places its own row's, each by 8 lanes (4 with more than
+  // 8 beams).
   const int sh = K > 8 ? 2 : 3, lanes = 1 << sh;
   const int c = lane >> sh;
   const int me = k * C + min(c, C - 1);
   const double ms = cand_score[me];
-  const uint64_t ma = cand_at[me];
   int place = 0;
   for (int j = lane & (lanes - 1); j < K * C; j += lanes) {
     const double s = cand_score[j];
-    const uint64_t t = cand_at[j];
-    place += s > ms || (s == ms && (t < ma || (t == ma && j < me)));
+    place += s > ms || (s == ms && j < me);
   }
   for (int m = lanes >> 1; m >= 1; m >>= 1) place += __shfl_xor(place, m);
   if (c < C && (lane & (lanes - 1)) == 0 && place < K) {
     // (the clamp keeps a wrong candidate in range)
-    const int token = (int)min((uint32_t)ma, (uint32_t)(V - 1));
+    const int token = (int)min(cand_token[me], (uint32_t)(V - 1));
     const int64_t o = (int64_t)g * K + place;
     a.out_scores[o] = (float)ms;
     a.out_tokens[o] = token;

@@ -47,3 +47,22 @@ def test_select_of_large_equal_logits(dtype, top, n):
         w = float(score - log_n)
         assert abs(float(scores[0, i]) - w) <= 2.0 ** -24 * abs(w) + 2.0 ** -20
         assert (int(parents[0, i]), int(tokens[0, i])) == (beam, token)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("beams", [1, 2])
+def test_select_orders_logits_whose_scores_are_equal(dtype, beams):
+    """Logits of 2^-60 and less beside one of 5: their scores are the same
+    number in 64 bits, but within a beam the larger logit comes first."""
+    K, V = 6, 40
+    x = torch.exp2(torch.arange(V, dtype=torch.float64) - 100).to(dtype)
+    x[3] = 5
+    x = x.expand(1, K, V).contiguous().to(DEV)
+    s = torch.full((1, K), -float("inf"), device=DEV)
+    s[0, 1:1 + beams] = -2.0
+    _, tokens, parents, _ = kda.beam_select(x, s)
+    torch.cuda.synchronize()
+    tokens, parents = tokens[0].tolist(), parents[0].tolist()
+    n = K - beams
+    assert tokens == [3] * beams + [V - 1 - i for i in range(n)]
+    assert parents == [1 + i for i in range(beams)] + [1] * n
