@@ -391,19 +391,19 @@ __global__ __launch_bounds__(64 * kBeamMax) void beam_pick_kernel(const BeamSele
           }
         }
         // wanted: better than the last of the list, and not in it already
-        bool wanted = false;
 #pragma unroll
-        for (int j = 0; j <= U; ++j) {
+        for (int j = 0; j <= U; ++j)
           if (key[j] <= least) key[j] = 0;
-          wanted |= key[j] != 0;
-        }
-        if (!__any(wanted)) continue;
         for (int c = 0; c < C; ++c) {
           const uint64_t have = __shfl((unsigned long long)list, c);
 #pragma unroll
           for (int j = 0; j <= U; ++j)
             if (key[j] == have) key[j] = 0;
         }
+        bool wanted = false;
+#pragma unroll
+        for (int j = 0; j <= U; ++j) wanted |= key[j] != 0;
+        if (!__any(wanted)) continue;
         uint64_t keep = 0;
         uint64_t before = ~0ull;
         for (int c = 0; c < C; ++c) {

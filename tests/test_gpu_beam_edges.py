@@ -66,3 +66,21 @@ def test_select_orders_logits_whose_scores_are_equal(dtype, beams):
     n = K - beams
     assert tokens == [3] * beams + [V - 1 - i for i in range(n)]
     assert parents == [1 + i for i in range(beams)] + [1] * n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [2, 5, 16])
+@pytest.mark.parametrize("V,gap", [(700, 1), (700, 64), (40000, 1), (40000, 8), (40000, 2048 * 8)])
+def test_select_whose_best_share_parts_or_do_not(dtype, K, V, gap):
+    """A row's best tokens next to one another (in one thread's part of the
+    row), and `gap` tokens apart; the best of all in the last beam."""
+    g = torch.Generator().manual_seed(V + K + gap)
+    x = torch.randn(1, K, V, generator=g).clamp(max=3).to(dtype)
+    at = (13 + gap * torch.arange(K + 2)) % V
+    x[0, :, at] = (8 + 0.25 * torch.randperm(K + 2, generator=g)).to(dtype)
+    s = torch.full((1, K), -60.0)
+    s[0, K - 1] = -1.0
+    _, tokens, parents, _ = kda.beam_select(x.to(DEV), s.to(DEV))
+    torch.cuda.synchronize()
+    want = x[0, K - 1].double().sort(descending=True, stable=True).indices[:K]
+    assert tokens[0].tolist() == want.tolist() and parents[0].tolist() == [K - 1] * K
