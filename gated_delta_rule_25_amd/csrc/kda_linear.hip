@@ -403,6 +403,14 @@ struct WalkLayout {
   static constexpr int BYTES = RC + (DK ? 2 * C * 4 : 0);
 };
 
+// 2^x of a sum of decays.  Its whole part goes into the exponent, as fp32 would
+// keep an x of 30 to 2^-19 only (1.3e-6 of the factor; the hardware's own
+// rounding is 2^-23).
+__device__ __forceinline__ float exp2_sum(double x) {
+  const double whole = __builtin_rint(fmax(x, -1000.0));  // (below 2^-1000 nothing is left in fp32)
+  return __builtin_amdgcn_ldexpf(exp2_fast((float)(fmax(x, -1000.0) - whole)), (int)whole);
+}
+
 // The state is kept as 2^s times what the accumulators hold, so that a chunk's
 // decay need not scale them: the decay wave moves it into s, and with it into
 // the factors of rows and tokens, until s falls below this (the factors stay
@@ -587,11 +595,11 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       const bool at_boundary = DG && --boundary == 0;  // the state behind the chunk is wanted
       if (at_boundary) boundary = stretch;
       if (scale < kScaleFloor || ci == nch - 1 || at_boundary) {
-        gam = exp2_fast((float)scale);
+        gam = exp2_sum(scale);
         scale = 0.0;
       }
-      const float row = exp2_fast((float)(before + (REV ? tot - s : s)));
-      const float wgt = exp2_fast((float)((REV ? s : tot - s) - scale));
+      const float row = exp2_sum(before + (REV ? tot - s : s));
+      const float wgt = exp2_sum((REV ? s : tot - s) - scale);
       const int b = ci & 3;
       if (lane < C) {
         const float hi = (float)s;
@@ -632,7 +640,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       chunk_barrier();
       if (nch > 0) finish(nch - 1);
     }
-    if (!OUT && lane == 0 && cb == 0) p.seg_decay[(size_t)slot * H + h] = exp2_fast((float)log_total);
+    if (!OUT && lane == 0 && cb == 0) p.seg_decay[(size_t)slot * H + h] = exp2_sum(log_total);
     return;
   }
 
