@@ -455,8 +455,7 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   constexpr int TN = Tok<E>::N;
   constexpr int C = L::C, NT = C / 16, ES = L::ES, NBUF = L::NBUF;
   constexpr bool BF = ES == 2;
-  constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values,
-  constexpr int MSV = OUT && !DG ? std::min(NSV, 2) : NSV;  // of which are always taken
+  constexpr int NSV = BF ? 3 : 1;              // terms of the weighted values
   constexpr int NSS = (BF && DG) ? 3 : 1;      // terms of the state in the outputs' product
   static_assert(L::BYTES <= 160 * 1024, "LDS budget exceeded");
   constexpr int KT = C / (4 * TN);             // token steps per chunk
@@ -886,9 +885,6 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
   load_x(0);
   chunk_barrier();  // iteration -1: the pair matrix of the first chunk is being formed
 
-  // A state that only bf16 outputs are taken from needs no third term of the
-  // weighted values: two cut at 16 bits are far below the outputs' rounding.
-  const bool fp32_state = DG || !OUT || (p.fin && (REV ? first : last));
   uint32_t base = lds0;  // of the chunk's query and key tiles
   read_q(base, 0);
   read_q(base, 1);
@@ -946,17 +942,9 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     };
     auto add_to_state = [&](int kt) {
 #pragma unroll
-      for (int s = 0; s < NSV; ++s) {
-        if (s >= MSV) continue;
+      for (int s = 0; s < NSV; ++s)
 #pragma unroll
         for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][s]);
-      }
-    };
-    auto add_rest = [&](int kt) {
-      if constexpr (MSV < NSV)
-        if (fp32_state)
-#pragma unroll
-          for (int rt = 0; rt < 8; ++rt) accS[rt] = mma_tok(accS[rt], fk[rt], fw[kt][NSV - 1]);
     };
     f32x4 accO[OUT ? NT : 1];
     if constexpr (OUT) {
@@ -1054,18 +1042,16 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     static_assert(KT == 2, "two token steps a chunk");
     add_to_state(0);
     weigh_values(1);
-    if constexpr (MSV == NSV) read_k(1, 0, 8);
+    read_k(1, 0, 8);
     if constexpr (BF) {
 #pragma unroll
-      for (int i = 0; i < 8 * MSV; ++i) {
+      for (int i = 0; i < 8 * NSV; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        if (MSV == NSV && i >= 8 * (NSV - 1)) __builtin_amdgcn_sched_group_barrier(0x100, Tok<E>::READS, 0);
+        if (i >= 8 * (NSV - 1)) __builtin_amdgcn_sched_group_barrier(0x100, Tok<E>::READS, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    add_rest(0);
-    if constexpr (MSV < NSV) read_k(1, 0, 8);
     if constexpr (OUT) {
       // rows behind the end fall outside the buffer view and are dropped
       const Rsrc orb = make_rsrc(static_cast<char*>(p.o) + ((size_t)t0 * H + h) * (D * oes),
@@ -1083,7 +1069,6 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       }
     }
     add_to_state(1);
-    add_rest(1);
     read_q(base_next, 0);
     read_q(base_next, 1);
     base = base_next;

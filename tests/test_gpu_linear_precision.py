@@ -166,3 +166,21 @@ def test_backward_states_and_decays(dtype, decay, case):
     else:
         r["dg"] = ratio(dg, w["dg"], bound.sum().sqrt())
     check(r)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,h,seg", [([200], 2, -1), ([300, 5, 70], 70, 0), ([500, 130], 2, 64), ([2100], 1, 0)])
+def test_bits_do_not_depend_on_which_states_are_wanted(dtype, lengths, h, seg):
+    """The outputs with and without the final state, and the gradients with
+    and without the initial state's."""
+    d = lt.make(lengths, h, h, dtype, "token", True, 33, DEV)
+    args = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, _ = kda.linear_chunk_fwd(*args, d["initial_state"], d["cu_seqlens"], segment_tokens=seg)
+    o2, none = kda.linear_chunk_fwd(*args, d["initial_state"], d["cu_seqlens"], segment_tokens=seg,
+                                    output_final_state=False)
+    assert none is None and torch.equal(o, o2)
+    a = kda.linear_chunk_bwd(*args, d["d_o"], d["initial_state"], d["cu_seqlens"], d["d_final_state"],
+                             segment_tokens=seg)
+    b = kda.linear_chunk_bwd(*args, d["d_o"], d["initial_state"], d["cu_seqlens"], d["d_final_state"],
+                             segment_tokens=seg, need_d_initial_state=False)
+    assert b[4] is None and all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
