@@ -911,7 +911,8 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     if (NW == 8 && wv >= 4) __builtin_amdgcn_s_setprio(1);
     const uint32_t base_next = base + L::SET == lds0 + NBUF * L::SET ? lds0 : base + L::SET;
     const uint32_t vbase = lds0 + L::VALS + (ci & 1) * L::VTILE;
-    const float gam = sGam[b];
+    // (in a scalar register)
+    const float gam = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sGam[b])));
     float w[KT][TN];
     TF fv[KT], fk[8];
     auto read_values = [&](int kt) {
@@ -1001,6 +1002,14 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) accO[rt] *= row[rt];
+      if (gam == 0.f) {
+        // the state is dropped in this chunk: rows behind that do not see it,
+        // whatever it holds (infinities and NaN times zero would be NaN)
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) accO[rt][i] = row[rt] == 0.f ? 0.f : accO[rt][i];
+      }
       if constexpr (DG) {
         float dot[NT];
 #pragma unroll
@@ -1031,9 +1040,13 @@ __device__ __forceinline__ void walk(const LinearWalkArgs& p, unsigned char* sme
     }
     if (NW == 8 && wv >= 4) __builtin_amdgcn_s_setprio(0);
     // the state's scale, when the decays have run far enough (decay wave)
-    if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gam)) != 0x3f800000) {
+    if (gam != 1.f) {
 #pragma unroll
       for (int rt = 0; rt < 8; ++rt) accS[rt] *= gam;
+      if (gam == 0.f) {
+#pragma unroll
+        for (int rt = 0; rt < 8; ++rt) accS[rt] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      }
     }
     // State.  The first step's products cover the second one's weighted values
     // and, as its keys come free, their reads; the second step's cover the
@@ -1363,7 +1376,7 @@ __device__ __forceinline__ void scan(const LinearScanArgs& a, int64_t block) {
       dec = a.seg_decay[where(j + 1)];
     }
     *reinterpret_cast<f32x4*>(a.snap + where(j) * kState + at) = s;
-    s = s * d + add;
+    s = d == 0.f ? add : s * d + add;  // (a dropped state may hold anything)
   }
 }
 

@@ -37,6 +37,10 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearDecodeAr
 #pragma unroll
   for (int i = 0; i < R; ++i) st[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + i * D));
   const float a = __expf(p.decay_per_head ? p.log_decay[h] : p.log_decay[u]);
+  if (a == 0.f) {  // the state is dropped, whatever it holds (infinities and NaN times zero would be NaN)
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  }
   const E* v = static_cast<const E*>(p.v) + u * D + col;
   const E* q = static_cast<const E*>(p.q) + uq * D + R * rg;
   const E* k = static_cast<const E*>(p.k) + uq * D + R * rg;

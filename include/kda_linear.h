@@ -21,8 +21,8 @@
  *   v, o        [T_total, num_heads, 128] dtype
  *   log_decay   [T_total, num_heads] fp32, or [num_heads] fp32 when
  *               decay_per_head is nonzero.  Any value <= 0, -inf included
- *               (the state is dropped before the token's write); positive
- *               values and NaN are outside the preconditions.
+ *               (the state is dropped before the token's write, whatever it
+ *               holds); positive values and NaN are outside the preconditions.
  *   states      [N, num_heads, 128, 128] fp32
  *
  * Preconditions not checked on the fast path: log_decay as above, q, k, v and
