@@ -126,26 +126,23 @@ def boundary_products(d, lengths, anchor):
     return out
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("decay", ["token", "head", "none", "reset"])
-@pytest.mark.parametrize("case", CASES, ids=lambda c: "%s-h%d-seg%d" % ("+".join(map(str, c[0])), c[1], c[2]))
-def test_backward_states_and_decays(dtype, decay, case):
-    lengths, h, seg = case
-    d = lt.make(lengths, h, h, dtype, decay, True, 32, DEV)
-    dq, dk, dv, dg, ds = kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["d_o"], d["initial_state"],
-                                              d["cu_seqlens"], d["d_final_state"], segment_tokens=seg)
+def gradient_ratios(d, got, lengths, dtype, cut):
+    """Errors of linear_chunk_bwd's results over their bounds; d as lt.make gives it."""
+    dq, dk, dv, dg, ds = got
+    h, per_head = d["v"].shape[1], d["log_decay"].dim() == 1
     w = lt.backward(d["q"], d["k"], d["v"], d["log_decay"], d["d_o"], d["initial_state"], lengths, d["d_final_state"])
-    cut = segment_of(lengths, h, seg, True)
-    anchor = anchor_of(cut, decay == "head")
+    anchor = anchor_of(cut, per_head)
     r = {}
     for i, T in enumerate(lengths):
         n = steps(T, dtype, cut)
         for j in range(h):
             r["dS%d.%d" % (i, j)] = ratio(ds[i, j], w["ds0"][i, j], (5 + n) ** 0.5 * U * w["ds0"][i, j].norm())
     n = steps(max(lengths), dtype, cut)
-    if dtype == "f32":
-        for name, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+    for name, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+        if dtype == "f32":
             r[name] = ratio(x, w[name], (5 + n + 77) ** 0.5 * U * w[name].norm())
+        else:  # three roundings to bf16: the result, the pair matrix, the state as an operand
+            r[name] = ratio(x, w[name], 3 ** 0.5 * 2.0 ** -8 * w[name].norm())
     q, k = d["q"].cpu().double(), d["k"].cpu().double()
     own = (q * w["dq"]).sum(-1).square() + (k * w["dk"]).sum(-1).square()
     rc = own + ((q.norm(dim=-1) * w["dq"].norm(dim=-1)).square() + (k.norm(dim=-1) * w["dk"].norm(dim=-1)).square()) / 128
@@ -155,7 +152,7 @@ def test_backward_states_and_decays(dtype, decay, case):
         at[b:b + len(x)] += x.sum(0)
         b += len(x)
     bound = (5 + n + 77) * (lt.suffix_within(rc, lengths, anchor) + at) * U * U + (U * w["dg"]).square()
-    if decay == "head":
+    if per_head:
         # the tokens' sums: those of a stretch share what is behind them, so they add up as they are
         total = 0.0
         for x in per_sequence(bound.sqrt(), lengths):
@@ -165,6 +162,44 @@ def test_backward_states_and_decays(dtype, decay, case):
         r["dg"] = ratio(dg, want, (total + (U * want).square()).sum().sqrt())
     else:
         r["dg"] = ratio(dg, w["dg"], bound.sum().sqrt())
+    return r
+
+
+def backward(d, seg):
+    return kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["d_o"], d["initial_state"], d["cu_seqlens"],
+                                d["d_final_state"], segment_tokens=seg)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", ["token", "head", "none", "reset"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "%s-h%d-seg%d" % ("+".join(map(str, c[0])), c[1], c[2]))
+def test_backward_states_and_decays(dtype, decay, case):
+    lengths, h, seg = case
+    d = lt.make(lengths, h, h, dtype, decay, True, 32, DEV)
+    check(gradient_ratios(d, backward(d, seg), lengths, dtype, segment_of(lengths, h, seg, True)))
+
+
+# One sequence whose last dv walks take half heads, several ordered by length in
+# whole and in half heads, whole heads in a walk each: as the library chooses.
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("lengths,h,heads", [([1100], 90, [0, 75, 76, 89]), ([3, 700, 1500, 0, 64], 70, [0, 69]),
+                                             ([900, 5, 1030], 40, [0, 39]), ([1050, 1050], 128, [0, 127])])
+def test_schedules_of_many_heads_over_several_stretches(lengths, h, heads, decay):
+    """The heads are independent: some of them against the definition."""
+    d = lt.make(lengths, h, h, "bf16", decay, True, 34, DEV)
+    assert segment_of(lengths, h, 0, True) is None
+    o, fin = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["initial_state"], d["cu_seqlens"])
+    got = backward(d, 0)
+    torch.cuda.synchronize()
+    dim = {"log_decay": -1}
+    one = {n: None if x is None else x if n == "cu_seqlens" else
+           x.cpu().index_select(dim.get(n, 1), torch.tensor(heads)) for n, x in d.items()}
+    part = [x[..., heads] if i == 3 else x[:, heads] for i, x in enumerate(got)]
+    r = gradient_ratios(one, part, lengths, "bf16", None)
+    want, wfin = lt.forward(one["q"], one["k"], one["v"], one["log_decay"], one["initial_state"], lengths)
+    r["o"] = ratio(o[:, heads], want, 3 ** 0.5 * 2.0 ** -8 * want.norm())
+    r["S"] = max(ratio(fin[i, h], wfin[i, j], (5 + steps(T, "bf16", None)) ** 0.5 * U * wfin[i, j].norm())
+                 for i, T in enumerate(lengths) for j, h in enumerate(heads))
     check(r)
 
 
