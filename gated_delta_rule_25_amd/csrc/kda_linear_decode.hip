@@ -7,7 +7,7 @@
 // them and keeps the products with q_i; nothing of the new state depends on a
 // sum over the old one, so stores follow their own loads with no barrier
 // between.  Bound by HBM: 128 KiB of state per (sequence, head) and step
-// against 4 x 128^2 flops (256 sequences x 96 heads: 568 us, 5.7 TB/s).
+// against 4 x 128^2 flops (256 sequences x 96 heads: 550 us, 5.9 TB/s).
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_internal.h"
@@ -37,10 +37,10 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearDecodeAr
 #pragma unroll
   for (int i = 0; i < R; ++i) st[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + i * D));
   const float a = __expf(p.decay_per_head ? p.log_decay[h] : p.log_decay[u]);
-  if (a == 0.f) {  // the state is dropped, whatever it holds (infinities and NaN times zero would be NaN)
-#pragma unroll
-    for (int i = 0; i < R; ++i) st[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  }
+  // a zero drops the state, whatever it holds (infinities and NaN times zero
+  // would be NaN); chosen element by element, as a branch would wait for all of
+  // the state (256 sequences x 96 heads: 550 us, with a branch 572)
+  const bool keep = a != 0.f;
   const E* v = static_cast<const E*>(p.v) + u * D + col;
   const E* q = static_cast<const E*>(p.q) + uq * D + R * rg;
   const E* k = static_cast<const E*>(p.k) + uq * D + R * rg;
@@ -48,7 +48,10 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(const LinearDecodeAr
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const f32x4 ns = a * st[i] + to_f32(k[i]) * vv;
+    f32x4 old = a * st[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) old[j] = keep ? old[j] : 0.f;
+    const f32x4 ns = old + to_f32(k[i]) * vv;
     __builtin_nontemporal_store(ns, reinterpret_cast<f32x4*>(S + i * D));
     o += to_f32(q[i]) * ns;
   }
@@ -80,7 +83,8 @@ hipError_t launch_decode_s(const LinearDecodeArgs& a, hipStream_t stream) {
 // Up to here the states fit the 256 MiB cache in front of HBM, and four
 // workgroups for each keep more loads in flight (1 x 32 heads: 3.1 us against
 // 5.1; 4 x 96: 6.3 against 10.9; 32 x 96: 75 against 78); beyond, rows of 128
-// bytes cost more than whole ones (256 x 96: 614 us against 568).
+// bytes cost more than whole ones (256 x 96: 614 us against 568 when this was
+// chosen).
 constexpr int64_t kSplitUnits = 4096;
 
 template <typename E>
