@@ -15,15 +15,17 @@
 //   beam_scan_kernel   reads every logit once: per thread the largest element
 //                      of its part and, rescaled to the workgroup's maximum,
 //                      the sum of exponentials (exponentials of differences
-//                      to the thread's own maximum, fp32; combined in fp64).
+//                      to the thread's own maximum, fp32; the workgroup's
+//                      threads are combined in fp64, and its sum kept in fp32:
+//                      half a step, 6e-8, of what the score takes the log of).
 //                      Bound by HBM (64 groups x 8 beams x 128003 bf16 logits:
 //                      28 us, 4.7 TB/s).
 //   beam_pick_kernel   one workgroup per group: the K best parts of each row,
 //                      their elements read again (K x nv vectors), the row's
 //                      K best; then the K best of the K x K candidates,
 //                      compared as fp64 scores.  Bound by latency: a chain of
-//                      dependent reads and counts (the same case: 14 us; one
-//                      group of 4 beams x 32000: 8 us after a scan of 4.5).
+//                      dependent reads and counts (the same case: 13 us; one
+//                      group of 4 beams x 32000: 7 us after a scan of 4.5).
 // Nothing depends on the order in which workgroups run.
 //
 // Reordering.  Row n of a group's states becomes the row of its parent.  A

@@ -20,15 +20,18 @@
 // token boundary equals <S, dS>.  The dq walk leaves the r_t and the dk walk
 // the c_t, and both the states at every boundary of `anchor` tokens; the sum
 // over t is restarted from their product there, so that rounding cannot build
-// up along the sequence (linear_decay_grad_kernel).
+// up along the sequence (decay_grad, in linear_finish_kernel).
 //
 // What is rounded.  bf16: the pair matrix (q_i . k_j) e^{..} and the state,
 // as operands of the outputs' products, to one bf16 each (the output is bf16
 // itself: measured 2.3e-3 of its norm off the 64-bit result, against 1.7e-3 for
-// the output's own rounding).  The state's update takes e^{..} v_j as the sum
-// of three bf16 terms (24 bits), because the state is an fp32 result; the
-// part of r_t and c_t that comes through the state takes three terms of the
-// state for the same reason.  Accumulation is fp32, prefix sums of the decays
+// the output's own rounding; a second term of each does not fit LDS in the
+// walks of whole heads).  The state's update takes e^{..} v_j as the sum
+// of three bf16 terms (24 bits), because the state is an fp32 result, and in
+// every walk, so that no output's bits depend on whether the state is asked
+// for; the part of r_t and c_t that comes through the state takes three terms
+// of the state for the same reason (and with it dq and dk where the decays'
+// gradient is wanted, else they take one).  Accumulation is fp32, prefix sums of the decays
 // are fp64 (a difference of two sums decides every factor).
 #include <algorithm>
 #include <atomic>
@@ -442,7 +445,9 @@ constexpr double kScaleFloor = -30.0;
 // TB/s of the 4.8 that a large copy reaches here; copies and compute waves take
 // about 3500 cycles a chunk each.  Backward, whole heads: a dk, dq, dv walk of
 // 128 chunks takes 610, 590, 400 us side by side, 8700 cycles a chunk with the
-// decays' gradient where its matrix instructions take 3600 of a SIMD.
+// decays' gradient where its matrix instructions take 3600 of a SIMD.  The
+// three walks fetch 2.3 GB and write 0.72 GB, 620 us at a large copy's rate: at
+// 650-685 us the launch is as near to that bound as to the waves' own.
 // REV walks backwards in time: the pair matrix is upper triangular and the
 // factors of rows and of tokens change places.
 // DG (the decays' gradient): x is q in the dq walk and k in the dk walk.
@@ -1234,7 +1239,7 @@ hipError_t launch_grad_t(const LinearGradArgs& a, hipStream_t stream) {
   constexpr int THREADS = 64 * (NW + 4);
   const int64_t items = a.dq.units / a.dq.num_heads;
   const int per = GradGrid(a.dq.num_heads, 8 / NW, a.dv_whole).blocks;
-  const int64_t most = kMaxThreads / THREADS / per;  // items of a launch (65535 heads: 14)
+  const int64_t most = kMaxThreads / THREADS / per;  // items of a launch (65535 heads: 28, by half heads 21)
   LinearGradArgs part = a;
   for (part.item0 = 0; part.item0 < items; part.item0 += most) {
     const int64_t blocks = std::min(items - part.item0, most) * per;

@@ -56,18 +56,21 @@ struct LinearPlan {
 // against 4.7).
 //
 // Forward: segments, one per unit, from three units per chain on (8 heads x
-// 131072 tokens: 380 us in segments of 4096, 448 at 1024, 3726 in one walk; 96
-// heads x 8192: 225 us in one walk of half heads, 300 at 1536); half heads
+// 131072 tokens: 367 us in segments of 4096, 440 at 1024, 3250 in one walk; 96
+// heads x 8192: 226 us in one walk of half heads, 293 at 1536); half heads
 // when chains are fewer than units.
 // Backward, three walks a chain: segments, one per unit, from five units per
-// chain on (32 heads x 8192 tokens: 280 us in segments of 1024, 320 at 512, 333
-// in one walk of half heads; 48 heads: 443, 497 and 493 in one walk of whole
-// ones; 64 heads: 570, 633, 512).  With more chains one walk each: whole heads if all chains are as long
-// (96 heads x 8192: 700-727 us, half heads 975, segments of 1024 855).  The
-// lengths of several sequences are not known here, and the longest one is
-// waited for: half heads until two rounds of the card are full (9 sequences of
-// up to 2900 tokens x 16 heads: 157 us, whole heads 206; of up to 1200: 103
-// against 85).
+// chain on (32 heads x 8192 tokens: 290 us in segments of 1024, 338 at 512, 331
+// in one walk of half heads; 48 heads: 443, 510 and 468 in one walk of whole
+// ones; 64 heads: 573, 654, 518).  With more chains one walk each: whole heads
+// if all chains are as long (96 heads x 8192: 690 us, segments of 1024 873; half
+// heads 975 when this was chosen).  The lengths of several sequences are not
+// known here, and the longest one is waited for: half heads until two rounds of
+// the card are full (when this was chosen, 9 sequences of up to 2900 tokens x
+// 16 heads: 157 us, whole heads 206; of up to 1200: 103 against 85).
+// One rule for all sequences of a batch: one that is much longer than the rest
+// is walked alone unless segment_tokens cuts it (65536 tokens among 29 sequences
+// of 100 to 1136, 4 heads: 1560 us, 156 in segments of 2048).
 void choose_segments(LinearPlan& pl, int num_seqs, int64_t total_tokens, int num_heads, int segment_tokens, int cus,
                      bool backward) {
   const int64_t units = (int64_t)num_seqs * num_heads;

@@ -81,10 +81,9 @@ hipError_t launch_decode_s(const LinearDecodeArgs& a, hipStream_t stream) {
 }
 
 // Up to here the states fit the 256 MiB cache in front of HBM, and four
-// workgroups for each keep more loads in flight (1 x 32 heads: 3.1 us against
-// 5.1; 4 x 96: 6.3 against 10.9; 32 x 96: 75 against 78); beyond, rows of 128
-// bytes cost more than whole ones (256 x 96: 614 us against 568 when this was
-// chosen).
+// workgroups for each keep more loads in flight (1 x 32 heads: 2.8 us now, 3.1
+// against 5.1 when this was chosen; 4 x 96: 6.3 against 10.9; 32 x 96: 75 against 78); beyond, rows of 128
+// bytes cost more than whole ones (256 x 96: 614 us against 568).
 constexpr int64_t kSplitUnits = 4096;
 
 template <typename E>

@@ -162,7 +162,7 @@ def linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     log_decay and the initial state: dq and dk summed over the heads that
     share a query and key head, d_log_decay of a constant decay over all
     tokens.  The last two are None when not needed; without d_log_decay the
-    call does less work."""
+    call does less work (and bf16 dq and dk may differ in their last bit)."""
     lib = _load()
     n, t, h, hq, per_head = _sizes(q, k, v, log_decay, cu_seqlens, "T")
     dev, dt = q.device, q.dtype
@@ -241,7 +241,10 @@ def chunk_linear(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     one) and the initial state from linear_chunk_bwd, once (no gradients of
     gradients).  A graph capture has to hold the forward and the backward, with
     no output of an eager call with the same leaves alive: a backward that
-    would accumulate through such a call's nodes is refused."""
+    would accumulate through such a call's nodes is refused.  That is seen for
+    leaves that are arguments here and for calls of this function; leaves in
+    front of them, and graphs that other operations made of the same leaves, are
+    the caller's to free, as with any operation of torch."""
     o, final_state = _ChunkLinear.apply(q, k, v, log_decay, initial_state, cu_seqlens)
     _mark_accumulators(o)
     return o, final_state

@@ -25,15 +25,21 @@
  *               holds); positive values and NaN are outside the preconditions.
  *   states      [N, num_heads, 128, 128] fp32
  *
- * Preconditions not checked on the fast path: log_decay as above, q, k, v and
- * the gradients finite, cu_seqlens non-decreasing from 0 to total_tokens.
+ * Preconditions not checked on the fast path: log_decay as above; q, k, v and
+ * the gradients finite, and so are states that no decay of -inf drops before
+ * they are read; sums of k v^T below 2^97 (the walk holds up to 2^30 times the
+ * state); cu_seqlens non-decreasing from 0 to total_tokens.
  * Outside them the results are undefined but every access stays in bounds.
  * The device the stream belongs to has to be the current one.
  *
  * Accuracy.  fp32 results (fp32 I/O, states, d_log_decay) are computed to
- * fp32 accuracy also from bf16 inputs; bf16 results carry their own rounding
- * and that of the bf16 operands of the last product.  Every sum runs in a
- * fixed order: repeated calls give the same bits.
+ * fp32 accuracy also from bf16 inputs.  bf16 results of the chunk calls carry
+ * three roundings to bf16: their own, that of the products q . k as an operand
+ * of the last product, and that of the state as one (together 1.4 times the
+ * error of the first alone); those of the decode step only their own.  Every
+ * sum runs in a fixed order: repeated calls give the same bits, and o and dv do
+ * not depend on which states are asked for.  bf16 dq and dk may differ in
+ * their last bit with and without d_log_decay, which reads more of the state.
  */
 #ifndef KDA_LINEAR_H_
 #define KDA_LINEAR_H_
@@ -98,7 +104,8 @@ size_t kda_linear_chunk_bwd_workspace_bytes(int num_seqs, int64_t total_tokens, 
  *
  * It needs only the forward's inputs; no output may overlap an input, another
  * output or the workspace.  With d_log_decay, total_tokens * num_heads / 1024
- * (a constant decay: / 256) + 2 * num_seqs * num_heads is at most 14 * 2^20.
+ * (a constant decay: / 256; with segments the largest multiple of 64 up to that
+ * which divides their length) + 2 * num_seqs * num_heads is at most 14 * 2^20.
  */
 kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                                 const float* initial_state, const int32_t* cu_seqlens, const void* d_o,
