@@ -78,12 +78,16 @@ __device__ __forceinline__ void delta_walk(const DeltaWalkArgs& p, unsigned char
   {
     const float* src = nullptr;
     if (W != Walk::STATES) {
-      if (!it.first) src = p.pairs + ((size_t)(it.slot - 1) * H + h) * 2 * kState;
-      else if (p.init) src = p.init + nh * kState;
-      // a first decay that leaves nothing of the state drops it, whatever it holds
-      if (src && it.first && nch > 0 &&
-          exp2_sum((double)fmaxf(p.log_decay[(size_t)it.tb * H + h], kMinLogDecay) * kLog2e) == 0.f)
-        src = nullptr;
+      if (p.segmented && !(W == Walk::OUT && p.led && it.first)) {
+        // from the scan, the first segment's too: `fin` may be `init`, and a sequence's segments, the last of
+        // which writes `fin`, are walked in any order
+        src = p.pairs + ((size_t)it.entry * H + h) * 2 * kState;
+      } else {
+        if (p.init) src = p.init + nh * kState;
+        // a first decay that leaves nothing of the state drops it, whatever it holds
+        if (src && nch > 0 && exp2_sum((double)fmaxf(p.log_decay[(size_t)it.tb * H + h], kMinLogDecay) * kLog2e) == 0.f)
+          src = nullptr;
+      }
     }
 #pragma unroll
     for (int m = 0; m < M; ++m)
@@ -507,7 +511,9 @@ hipError_t launch_save_e(const DeltaWalkArgs& a, hipStream_t stream) {
 // in the layout of an fp32 result tile, which is the next product's operand;
 // the 128 x 16 tile goes through LDS after each step, and the next segment's M
 // and B are fetched while one step runs.  S_in(j+1) takes B_j's place; that of
-// segment 1 is there already where the first segments have been walked (led).
+// segment 1 is there already where the first segments have been walked (led), else
+// S_in(0), which the walk reads here as `fin` may be `init`, takes the place of the
+// last segment's contribution, which nothing reads.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void delta_scan_kernel(const DeltaScanArgs a) {
   constexpr size_t kState = (size_t)D * D;
@@ -520,23 +526,28 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(const DeltaScanArgs a) 
   int64_t bos, eos;
   seq_range(a.cu, n, a.total_tokens, bos, eos);
   const int count = (int)((eos - bos + a.seg - 1) / a.seg);
-  if (count == 0) return;
   const int from = a.led ? 1 : 0;
-  if (count <= from + 1) return;
+  if (a.led && count <= from + 1) return;
   const int64_t base = slot_of(n, bos, a.seg, 0);
   auto pair = [&](int j) { return a.pairs + ((size_t)(base + j) * H + h) * 2 * kState; };
   __shared__ f32x4 sS[8][64];
   auto row_of = [&](int q, int i) { return 16 * (2 * wv + q) + 4 * g + i; };
   const float* start = a.led ? pair(0) : a.init ? a.init + (size_t)nh * kState : nullptr;
   // (the first decay may drop the state, whatever it holds)
-  if (!a.led && exp2_sum((double)fmaxf(a.log_decay[(size_t)bos * H + h], kMinLogDecay) * kLog2e) == 0.f) start = nullptr;
+  if (!a.led && count > 0 && exp2_sum((double)fmaxf(a.log_decay[(size_t)bos * H + h], kMinLogDecay) * kLog2e) == 0.f)
+    start = nullptr;
+  float* entry = pair(max(count, 1) - 1);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     f32x4 s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = start ? start[row_of(q, i) * D + col] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      s[i] = start ? start[row_of(q, i) * D + col] : 0.f;
+      if (!a.led) entry[row_of(q, i) * D + col] = s[i];
+    }
     sS[2 * wv + q][lane] = s;
   }
+  if (count <= from + 1) return;
   __syncthreads();
   Frag16<float> mf[2][8];
   f32x4 bj[2];

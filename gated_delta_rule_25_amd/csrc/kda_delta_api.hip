@@ -217,7 +217,12 @@ hipError_t begin_walk(kda::DeltaWalkArgs& w, const DeltaPlan& pl, char* ws, hipS
   }
   if (!pl.segmented) return hipSuccess;
   w.pairs = reinterpret_cast<float*>(ws + pl.off_pairs);
-  hipError_t e = kda::launch_delta_pairs(w, stream);
+  kda::DeltaWalkArgs pairs = w;
+  if (!w.led) {
+    pairs.init = nullptr;
+    pairs.fin = nullptr;
+  }
+  hipError_t e = kda::launch_delta_pairs(pairs, stream);
   if (e != hipSuccess) return e;
   kda::DeltaScanArgs s;
   std::memset(&s, 0, sizeof(s));
@@ -230,6 +235,9 @@ hipError_t begin_walk(kda::DeltaWalkArgs& w, const DeltaPlan& pl, char* ws, hipS
   s.total_tokens = w.total_tokens;
   s.num_heads = w.num_heads;
   s.seg = w.seg;
+  // (the walk takes every state from the scan: a final state in the initial one's place is written by a
+  // sequence's last segment while its first one may yet have to begin)
+  w.init = nullptr;
   return kda::launch_delta_scan(s, stream);
 }
 

@@ -70,9 +70,11 @@ struct DeltaWalkArgs {
   int seg;                 // tokens per segment
   bool segmented;          // work items are (segment, head), else (sequence, head)
   int64_t unit0, units;    // work items (set by the launch)
-  const float* init;       // [N,H,128,128] or null (zero)
-  float* fin;              // [N,H,128,128] or null
-  float* pairs;            // [segment slots][H][2][128,128]: pairs pass (written), else the states at segments' ends
+  const float* init;       // [N,H,128,128] or null (zero); read where a sequence is walked whole, and by the pairs
+                           // pass (led)
+  float* fin;              // [N,H,128,128] or null; may be init: no launch that walks a sequence's first segment apart
+                           // from its last one may be given both
+  float* pairs;            // [segment slots][H][2][128,128]: pairs pass (written), else the states that enter segments
   bool all_pairs;          // pairs pass: of all segments, as the backward pass reads
   bool led;                // the pairs pass walks the first segments' outputs
   bool both;               // pairs pass: a workgroup walks a segment's contribution and its transition
@@ -81,8 +83,8 @@ struct DeltaWalkArgs {
 };
 
 struct DeltaScanArgs {
-  float* pairs;            // contributions and transitions in, states at segments' ends (in the contributions' place) out
-  bool led;                // the first segments' are there
+  float* pairs;            // contributions and transitions in, states that enter segments (in contributions' places) out
+  bool led;                // the first segments have been walked; else what enters them is written too
   const float* init;
   const float* log_decay;
   const int32_t* cu;

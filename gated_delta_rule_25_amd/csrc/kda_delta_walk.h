@@ -79,6 +79,7 @@ constexpr bool is_back(Walk w) { return w == Walk::BACK || w == Walk::BACK_STATE
 struct Item {
   int h, n;
   int64_t bos, eos, tb, te, slot;
+  int64_t entry;     // segments: the slot in which delta_scan_kernel leaves the state that enters this one
   bool first, last;  // it begins / ends its sequence
   bool ok;
   int nch;           // chunks
@@ -101,10 +102,11 @@ __device__ __forceinline__ Item find_item(const A& p, unsigned char* smem, int64
     it.te = min(s.eos, it.tb + p.seg);
     it.first = s.j == 0;
     it.last = s.j + 1 >= s.count;
+    it.entry = it.first ? rank + max(s.count, 1) - 1 : rank - 1;
   } else {
     it.n = longest_first<kWalkThreads>(reinterpret_cast<int*>(smem), p.cu, p.num_seqs, p.total_tokens, (int)rank);
     seq_range(p.cu, it.n, p.total_tokens, it.bos, it.eos);
-    it.slot = 0;
+    it.slot = it.entry = 0;
     it.tb = it.bos;
     it.te = it.eos;
     it.first = it.last = true;
