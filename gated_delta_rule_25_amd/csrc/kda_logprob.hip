@@ -15,7 +15,8 @@
 // the chain of loads, reductions and reads where few (4 of 32000 fp32: 12 us).
 //
 // Backward: elementwise, one read and one write of the row (none where nothing
-// reaches it).  Bound by HBM (4096 rows of 128003 bf16: 433 us, 4.8 TB/s).
+// reaches it; one more read where log s is lost beside the largest logit, below).
+// Bound by HBM (4096 rows of 128003 bf16: 433 us, 4.8 TB/s).
 #include <algorithm>
 
 #include "kda_logits.h"
@@ -254,11 +255,86 @@ __global__ __launch_bounds__(THREADS) void logprob_kernel(const LogprobArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
+// log p = x - z is off by half a step of z, and p by as much of itself: 2^-15 of it
+// where |z| is below this, in bf16 (whose results are rounded to 2^-9) 2^-13.  Logits
+// that are all as large as that are rare, and then one step of z may be more than
+// log s: a row filled with its type's lowest value would get p = 1 for every token.
+// Farther out one of a row's workgroups reads it once more, finds its largest m and
+// log s, and takes it alone, as d_logits may be the logits: log p = (x - m) - log s.
+// (4096 such rows of 128003 bf16: 1.30 ms, others 0.44; one row 35 us for 5.6.)
+template <typename E>
+constexpr float kFar = sizeof(E) == 2 ? 4096.f : 1024.f;
+
+// m and log s of a row that is not masked throughout; every thread's reads have
+// ended.  What they make is taken only if it is z: else z is what the caller wants.
+template <typename E>
+__device__ __forceinline__ void largest_and_sum(const E* x, const BeamRow& r, int V, float z, float& top, float& log_s) {
+  constexpr int U = 16 / (int)sizeof(E), WAVES = kGradThreads / 64;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  float m = -INFINITY;
+  double s = 0.0;
+  // N vectors, or what there is of them
+  auto take = [&](const auto& v) {
+    constexpr int N = sizeof(v) / sizeof(float);
+    const float* y = &v[0][0];
+    float vm = y[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) vm = fmaxf(vm, y[j]);
+    if (vm > m) {
+      s *= (double)beam_exp(fmaxf(m - vm, kLeast));
+      m = vm;
+    }
+    if (m == -INFINITY) return;
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) part += beam_exp(fmaxf(y[j] - m, kLeast));
+    s += (double)part;
+  };
+  int vec = t;
+  for (; vec + 3 * kGradThreads < r.nvec; vec += 4 * kGradThreads) {
+    float v[4][U];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_vector<E>(v[i], x + r.head + (int64_t)(vec + i * kGradThreads) * U);
+    take(v);
+  }
+  for (; vec < r.nvec; vec += kGradThreads) {
+    float v[1][U];
+    load_vector<E>(v[0], x + r.head + (int64_t)vec * U);
+    take(v);
+  }
+  const int i = beam_extra<E>(r, V, t);
+  if (i >= 0) {
+    const float v[1][1] = {{load_logit(x + i)}};
+    take(v);
+  }
+  __shared__ float sm[WAVES];
+  __shared__ double ss[WAVES];
+  const float wm = wave_fmax(m);
+  if (lane == 0) sm[wv] = wm;
+  __syncthreads();
+  float all = sm[0];
+#pragma unroll
+  for (int k = 1; k < WAVES; ++k) all = fmaxf(all, sm[k]);
+  s *= m > -INFINITY ? (double)beam_exp(fmaxf(m - all, kLeast)) : 0.0;
+#pragma unroll
+  for (int k = 32; k >= 1; k >>= 1) s += __shfl_xor(s, k);
+  if (lane == 0) ss[wv] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) s += ss[k];
+  const double l = log(s);
+  if (fabs((double)all + l - (double)z) <= fabs((double)z) * 0x1p-23) {
+    top = all;
+    log_s = (float)l;
+  }
+}
+
 template <typename E>
 __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(const LogprobGradArgs a) {
   constexpr int U = 16 / (int)sizeof(E);
   const int64_t row = a.row0 + blockIdx.x / a.slices;
-  const int slice = (int)(blockIdx.x % a.slices);
+  int slice = (int)(blockIdx.x % a.slices);
   const int V = a.vocab;
   const E* x = static_cast<const E*>(a.logits) + row * a.row_stride;
   E* dx = static_cast<E*>(a.d_logits) + row * a.d_row_stride;
@@ -270,23 +346,29 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(const Logpro
   const float h = any && a.d_entropy ? a.d_entropy[row] : 0.f;
   // -p (g + h (log p + entropy))
   const float c = h != 0.f ? g + h * a.entropy[row] : g;
+  float top = z, log_s = 0.f;  // z as a sum
   auto grad = [&](float v, int i) {
-    const float d = fmaxf(v - z, kLeast);
+    const float d = fmaxf((v - top) - log_s, kLeast);
     const float y = -beam_exp(d) * (c + h * d);
     return i == token ? y + g : y;
   };
   const bool zero = g == 0.f && h == 0.f;
   const BeamRow r = beam_row(x, V);
   const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
-  const int stride = kGradThreads * a.slices;
-  for (int vec = slice * kGradThreads + threadIdx.x; vec < r.nvec; vec += stride) {
-    const int e0 = r.head + vec * U;
-    float v[U];
+  const bool far = !zero && fabsf(z) >= kFar<E>;
+  const int stride = far ? kGradThreads : kGradThreads * a.slices;
+  if (far) {
+    // (another of each row's, for all XCDs to have their part)
+    if (slice != (int)(row % a.slices)) return;
+    slice = 0;
+    largest_and_sum(x, r, V, z, top, log_s);
+  }
+  int vec = slice * kGradThreads + threadIdx.x;
+  auto put = [&](float (&v)[U], int e0) {
     if (zero) {
 #pragma unroll
       for (int j = 0; j < U; ++j) v[j] = 0.f;
     } else {
-      load_vector<E>(v, x + e0);
 #pragma unroll
       for (int j = 0; j < U; ++j) v[j] = grad(v[j], e0 + j);
     }
@@ -307,6 +389,20 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(const Logpro
 #pragma unroll
       for (int j = 0; j < U; ++j) dx[e0 + j] = from_f32<E>(v[j]);
     }
+  };
+  // (one workgroup: four vectors in flight)
+  if (far)
+    for (; vec + 3 * kGradThreads < r.nvec; vec += 4 * kGradThreads) {
+      float v[4][U];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_vector<E>(v[i], x + r.head + (vec + i * kGradThreads) * U);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put(v[i], r.head + (vec + i * kGradThreads) * U);
+    }
+  for (; vec < r.nvec; vec += stride) {
+    float v[U];
+    if (!zero) load_vector<E>(v, x + r.head + vec * U);
+    put(v, r.head + vec * U);
   }
   if (slice == 0) {
     const int i = beam_extra<E>(r, V, threadIdx.x);
