@@ -138,6 +138,11 @@ bool debug_checks() {
   return e && *e && std::strcmp(e, "0") != 0;
 }
 void set_check_flags(uint32_t flags) { t_check_flags = flags; }
+
+std::mutex& checks_mutex() {
+  static std::mutex m;
+  return m;
+}
 }  // namespace kda
 
 namespace {

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "kda.h"
 
@@ -80,5 +81,8 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // (kda_last_precondition_flags).
 bool debug_checks();
 void set_check_flags(uint32_t flags);
+// Held while checks run: the failed ones are collected in a word of the device, which
+// calls of several threads share.
+std::mutex& checks_mutex();
 
 }  // namespace kda

@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "kda.h"
+#include "kda_api_util.h"
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -77,6 +78,7 @@ __global__ __launch_bounds__(256) void check_cu_kernel(const int32_t* cu, int nu
 }  // namespace
 
 hipError_t run_checks(const CheckArgs& a, hipStream_t stream, uint32_t* flags) {
+  const std::lock_guard<std::mutex> lock(checks_mutex());
   *flags = 0;
   void* dflag = nullptr;
   hipError_t e = hipGetSymbolAddress(&dflag, HIP_SYMBOL(g_check_flags));

@@ -8,6 +8,7 @@
 // (sequence, head) and step against 7 x 128^2 flops; 256 sequences x 96 heads take
 // 532 us, 6.1 TB/s.
 #include "kda.h"
+#include "kda_api_util.h"
 #include "kda_delta_internal.h"
 #include "kda_device.h"
 #include "kda_internal.h"
@@ -154,6 +155,7 @@ hipError_t launch_delta_decode(const DeltaDecodeArgs& a, hipStream_t stream) {
 hipError_t run_delta_checks(const void* k, bool bf16, int64_t k_rows, const float* log_decay, const float* beta,
                             int64_t count, const int32_t* cu, int num_seqs, int64_t total_tokens, hipStream_t stream,
                             uint32_t* flags) {
+  const std::lock_guard<std::mutex> lock(checks_mutex());
   *flags = 0;
   void* dflag = nullptr;
   hipError_t e = hipGetSymbolAddress(&dflag, HIP_SYMBOL(g_delta_flags));

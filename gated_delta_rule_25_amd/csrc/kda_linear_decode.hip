@@ -9,6 +9,7 @@
 // between.  Bound by HBM: 128 KiB of state per (sequence, head) and step
 // against 4 x 128^2 flops (256 sequences x 96 heads: 550 us, 5.9 TB/s).
 #include "kda.h"
+#include "kda_api_util.h"
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "kda_linear_internal.h"
@@ -118,6 +119,7 @@ hipError_t launch_linear_decode(const LinearDecodeArgs& a, hipStream_t stream) {
 
 hipError_t run_linear_checks(const float* log_decay, int64_t count, const int32_t* cu, int num_seqs,
                              int64_t total_tokens, hipStream_t stream, uint32_t* flags) {
+  const std::lock_guard<std::mutex> lock(checks_mutex());
   *flags = 0;
   void* dflag = nullptr;
   hipError_t e = hipGetSymbolAddress(&dflag, HIP_SYMBOL(g_linear_flags));
