@@ -39,7 +39,7 @@ struct DeltaPrepArgs {
   int num_heads, qk_heads;
   bool bf16;
   char* blocks;            // [chunk slots][H] blocks (written)
-  int64_t unit0, units;    // (chunk slot, head) of the launch (set by it)
+  int64_t unit0;           // first (chunk slot, head) of the launch (set by it)
 };
 
 // What the forward walk leaves for the backward pass.

@@ -13,8 +13,8 @@
 // and block column b downwards, X_ab = D_a (A_ab - sum_{b<=c<a} A_ac B_c X_cb),
 // on fp32 matrix cores, whose result tile is the next product's operand.
 //
-// Near HBM's rate: 96 heads x 8192 tokens take 86 us for 16 KiB read and 14 KiB
-// written per 64 tokens and head, 4.4 TB/s, with five workgroups a compute unit (as
+// Near HBM's rate: 96 heads x 8192 tokens take 86 us for 16.5 KiB read and 11.5 KiB
+// written per 64 tokens and head, 4.1 TB/s, with five workgroups a compute unit (as
 // LDS allows).  With the rows of A read all before the solve, 170 registers a wave,
 // there were three, and 111 us; before that two, and 144.
 #include <algorithm>
@@ -227,8 +227,7 @@ hipError_t launch_prep_e(DeltaPrepArgs a, hipStream_t stream) {
   constexpr int64_t MOST = kMaxThreads / L::THREADS;
   for (int64_t u = 0; u < units; u += MOST) {
     a.unit0 = u;
-    a.units = std::min(units - u, MOST);
-    hipLaunchKernelGGL(delta_prep_kernel<E>, dim3((unsigned)a.units), dim3(L::THREADS), 0, stream, a);
+    hipLaunchKernelGGL(delta_prep_kernel<E>, dim3((unsigned)std::min(units - u, MOST)), dim3(L::THREADS), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
