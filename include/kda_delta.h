@@ -39,7 +39,8 @@
  * the state and of the chunk's beta v, a chunk being up to 64 tokens, later ones
  * included (backwards: of dS, and of d_o times the largest of its row of q): an
  * output may be off by 2^-19 of that largest times its row of q, however small
- * it is itself.  bf16 results are off by their own rounding besides, 1.7e-3 in norm;
+ * it is itself, and so may the state be that a chunk leaves to the next one, from
+ * where on that decays as the state does.  bf16 results are off by their own rounding besides, 1.7e-3 in norm;
  * dq and dk, some of whose operands are fp16, by up to 3e-3 where keys are
  * nearly the same through a chunk and beta is near 1.  A decay below
  * 2^-126 counts as zero.  Every sum runs in a fixed order: repeated calls give

@@ -5,7 +5,9 @@ chunk's decays all but remove.
 Bounds.  Operands of a chunk are scaled by columns, by the largest m of what enters the
 chunk and of its beta v, later tokens included; what is off by their smallest step is at
 most 2^-19 m |q| of an output (delta_testlib), whatever the output's own size, and
-2^-18 m |q| with the products' and sums' parts, which are 2^-19 of values below m.
+2^-18 m |q| with the products' and sums' parts, which are 2^-19 of values below m.  The
+state that the chunk leaves is off by as much, so the next chunk's outputs are by twice
+that; later on it decays as the state does.
 
 Keys that are the same: with beta near 1 every u_j replaces what the ones before left,
 u_j = v_j - v_{j-1}, of sqrt(2) |v| where what remains is v.  bf16 dq and dk take u (and
@@ -99,7 +101,27 @@ def test_a_state_that_a_decay_within_the_chunk_removes(log_decay, dtype):
     if dtype == torch.bfloat16:
         lim = lim + 2.0 ** -8 * ref[0][at:, 0].abs()
     assert bool((err <= lim).all())
-    # (cut where the decay stands, the same tokens lose nothing to that state)
-    o2, _ = kda.delta_chunk_fwd(q[at:], k[at:], v[at:], la[at:], b[at:], torch.zeros_like(s0))
-    if log_decay == -math.inf:
-        check_forward(o2, None, forward(q[at:], k[at:], v[at:], la[at:], b[at:]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("scale", [10, 14])
+def test_what_a_removed_state_leaves_to_later_chunks(scale, dtype):
+    T, at = 200, 20
+    q, k, v, la, b, s0 = make(T, 1, 1, dtype, 67, decay=0.01)
+    s0.mul_(2.0 ** scale)
+    la[at] = -math.inf
+    o, fin = kda.delta_chunk_fwd(q, k, v, la, b, s0)
+    ref, ref_fin, _ = forward(q, k, v, la, b, s0)
+    m = s0[0, 0].abs().amax(0).cpu().double()
+    lim = q[:, 0].float().norm(dim=-1).cpu().double()[:, None] * 2.0 ** -17 * m
+    err = (o[:, 0].cpu().double() - ref[:, 0]).abs()
+    if dtype == torch.bfloat16:
+        lim = lim + 2.0 ** -8 * ref[:, 0].abs()
+    assert bool((err[at:] <= lim[at:]).all())
+    # (a column of the state: through a query of unit length)
+    assert bool(((fin.cpu().double() - ref_fin)[0, 0].norm(dim=0) <= 2.0 ** -17 * m).all())
+    # a sequence of its own from there on is off by nothing of it
+    cu = torch.tensor([0, at, T], dtype=torch.int32, device="cuda")
+    two = torch.cat([s0, torch.zeros_like(s0)])
+    o2, fin2 = kda.delta_chunk_fwd(q, k, v, la, b, two, cu)
+    check_forward(o2, fin2, forward(q, k, v, la, b, two, [at, T - at]))
