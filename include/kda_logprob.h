@@ -55,10 +55,12 @@ kda_status kda_token_logprobs_fwd(const void* logits, const int32_t* tokens, int
  *     d x_t = d_logprobs (1{t = token} - p_t) - d_entropy p_t (log p_t + entropy)
  *
  *   log_sum, entropy  the forward call's (entropy: with d_entropy, else ignored).
- *                     p is computed to 2^-14 of it (bf16: 2^-12), and to the
- *                     half step of log_sum where that is less, for logits of
- *                     any size: rows whose log_sum is 1024 (4096) or more in
- *                     size are read twice, by one workgroup each.
+ *                     p comes from x - log_sum in fp32: its relative error is
+ *                     half a step of log_sum, at most 2^-15 (bf16: 2^-13).
+ *                     Rows whose log_sum is 1024 (4096) or more in size are
+ *                     read once more, by one workgroup each, and p is taken
+ *                     relative to their largest logit; a log_sum that is not
+ *                     the row's own is taken as it is.
  *   d_logprobs    [rows] fp32; not read where the token is outside 0 .. vocab - 1
  *   d_entropy     [rows] fp32 or NULL (zero)
  *   d_logits      [rows, vocab] dtype, row r at d_logits + r * d_row_stride; may
